@@ -19,7 +19,9 @@ PROBE_LIB = os.path.join(PKG, "libep_probe.so")
 ARCH = "gfx950"
 
 SOURCES = ["layout.hip", "dispatch.hip", "fused.hip", "sources.hip", "nonexpand.hip",
-           "combine.hip", "overlap.hip", "api.cpp"]
+           "combine.hip", "overlap.hip", "api.cpp", "gate.hip", "experts.hip", "experts_bf16.hip",
+           "experts_mxfp4.hip", "experts_int4_g32.hip", "experts_int4_g64.hip",
+           "experts_int4_g128.hip", "moe_api.cpp"]
 PROBE_SOURCES = ["probe.hip"]
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 instructions.

@@ -12,6 +12,7 @@
 #include <mutex>
 #include <new>
 
+#include "ep_host.hpp"
 #include "ep_internal.hpp"
 
 // Workspace of the handles made by ep_handle_init_static, for callers that
@@ -27,19 +28,7 @@ namespace {
 
 thread_local char g_msg[512] = "";
 
-ep_status fail(ep_status st, const char* file, int line, const char* fmt, ...)
-{
-    char body[400];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(body, sizeof(body), fmt, ap);
-    va_end(ap);
-    const char* base = strrchr(file, '/');
-    snprintf(g_msg, sizeof(g_msg), "%s:%d %s", base ? base + 1 : file, line, body);
-    return st;
-}
-
-#define EP_FAIL(st, ...) fail((st), __FILE__, __LINE__, __VA_ARGS__)
+#define EP_FAIL(st, ...) epk::host_fail((st), __FILE__, __LINE__, __VA_ARGS__)
 #define EP_HIP(call)                                                                          \
     do {                                                                                      \
         hipError_t e_ = (call);                                                               \
@@ -225,6 +214,29 @@ struct ep_handle {
     template <typename T>
     T* at(int64_t off) const { return reinterpret_cast<T*>(ws + off); }
 };
+
+namespace epk {
+
+ep_status host_fail(ep_status st, const char* file, int line, const char* fmt, ...)
+{
+    char body[400];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(body, sizeof(body), fmt, ap);
+    va_end(ap);
+    const char* base = strrchr(file, '/');
+    snprintf(g_msg, sizeof(g_msg), "%s:%d %s", base ? base + 1 : file, line, body);
+    return st;
+}
+
+HandleInfo handle_info(const ep_handle* h)
+{
+    return HandleInfo{&h->cfg, h->num_tokens, h->pending, h->at<int32_t>(h->cv.psum_expert),
+                      h->at<int32_t>(h->cv.num_unaligned),
+                      h->at<uint32_t>(h->cv.ctrl) + kCtrlFlags};
+}
+
+}  // namespace epk
 
 namespace {
 

@@ -1,0 +1,11 @@
+// Products with INT4 weights with a scale per 64 columns: the kernels of product.hpp for this format.
+#include "product.hpp"
+
+namespace epk {
+
+hipError_t launch_product_int4_g64(const ProductArgs& a, int epilogue, hipStream_t s)
+{
+    return prod::launch_epilogue<kInt4G64>(a, epilogue, s);
+}
+
+}  // namespace epk
