@@ -55,7 +55,10 @@ struct ProductArgs {
     uint32_t* flags;
     // launch shape (set by launch_product)
     int kw;                     // waves of a block that share a tile's columns
-    int x_bytes;                // LDS for rows of x
+    int x_rows, x_bytes;        // rows of x in LDS at a time, and their bytes
+    int pass_rows;              // rows of an expert that are multiplied at once
+    uint32_t pass_magic;        // div_magic(pass_rows)
+    int dense_passes;           // ceil(num_rows / pass_rows)
 };
 
 struct ReduceArgs {

@@ -140,10 +140,12 @@ ep_status check_activation(const ep_weights* w, int32_t activation)
     return EP_OK;
 }
 
-ep_status check_rows(const void* d_x, int64_t rows, const void* d_y)
+ep_status check_rows(const ep_weights* w, const void* d_x, int64_t rows, const void* d_y)
 {
-    if (rows < 0 || rows >= (int64_t)1 << 31)
-        return EP_FAIL(EP_ERR_INVALID_ARG, "rows=%lld outside [0, 2^31)", (long long)rows);
+    // the kernels number (row, 16 outputs) tiles in 32 bits
+    if (rows < 0 || rows >= (int64_t)1 << 31 || rows * ((w->rows + 15) / 16) >= (int64_t)1 << 31)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "%lld rows times %d outputs outside [0, 2^35)",
+                       (long long)rows, w->rows);
     if (rows == 0) return EP_OK;
     if (!d_x || !d_y) return EP_FAIL(EP_ERR_INVALID_ARG, "x or y is NULL");
     if (!aligned(d_x, 16) || !aligned(d_y, 2))
@@ -242,7 +244,7 @@ ep_status ep_matvec(const ep_weights* w, const void* d_x, int64_t num_rows, int3
 {
     ep_status st = check_weights(w, "w", true);
     if (st == EP_OK) st = check_activation(w, activation);
-    if (st == EP_OK) st = check_rows(d_x, num_rows, d_y);
+    if (st == EP_OK) st = check_rows(w, d_x, num_rows, d_y);
     if (st != EP_OK) return st;
     if (w->num_experts != 1)
         return EP_FAIL(EP_ERR_INVALID_ARG, "ep_matvec takes one matrix (num_experts=%d)", w->num_experts);
@@ -266,7 +268,7 @@ ep_status ep_expert_matvec(const ep_handle* h, const ep_weights* w, const void* 
     if (!h) return EP_FAIL(EP_ERR_INVALID_ARG, "handle is NULL");
     ep_status st = check_weights(w, "w", true);
     if (st == EP_OK) st = check_activation(w, activation);
-    if (st == EP_OK) st = check_rows(d_x, x_rows, d_y);
+    if (st == EP_OK) st = check_rows(w, d_x, x_rows, d_y);
     if (st != EP_OK) return st;
     const epk::HandleInfo info = epk::handle_info(h);
     if (info.cfg->non_expand)

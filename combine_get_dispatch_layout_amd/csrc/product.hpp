@@ -40,8 +40,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4;            // per block
-constexpr int kThreads = kWaves * kWave;
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
 {
@@ -65,47 +63,118 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Weights and scales are read through a buffer resource per tile (its first
+// row as the base, its rows as the bound): the address of a load is one lane
+// offset that never changes and one scalar, so the loop has no address
+// arithmetic in vector registers.  (Offsets stay inside the tile: the bound
+// is no substitute for that where the scalar offset passes it.)
+typedef __amdgpu_buffer_rsrc_t Buffer;
+
+__device__ __forceinline__ Buffer make_buffer(const uint8_t* base, int64_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, (int)bytes, 0x00020000);
+}
+
+// Weights are read once: the non-temporal hint (aux bit 1) keeps them from
+// displacing x and the scales in the caches.
+constexpr int kNonTemporal = 2;
+
+__device__ __forceinline__ u32x4 load_weights(Buffer b, uint32_t lane_off, uint32_t off)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_off, off, kNonTemporal));
+}
+
 template <int KIND>
 struct Format {
     static constexpr bool kInt4 = KIND >= kInt4G32;
-    static constexpr int kSpan = KIND == kBf16 ? 32 : 128;      // columns of 64 bytes
+    static constexpr int kLine = KIND == kBf16 ? 64 : 256;      // columns of a line
     static constexpr int kParts = KIND == kBf16 ? 1 : 4;        // instructions of a span
-    // parts that share a scale (INT4)
-    static constexpr int kGroupParts = KIND == kInt4G32 ? 1 : KIND == kInt4G64 ? 2 : 4;
+    static constexpr int kGroup = KIND == kInt4G128 ? 128 : KIND == kInt4G64 ? 64 : 32;
+    // INT4: parts of a span that share a scale
+    static constexpr int kGroupParts = KIND == kInt4G128 ? 2 : 1;
+    // bytes of x: a line, and from one span, part and lane c to the next
+    static constexpr int kLineBytes = 2 * kLine;
+    static constexpr int kSpanBytes = KIND == kBf16 ? 16 : 64;
+    static constexpr int kPartBytes = kInt4 ? 128 : 16;
+    static constexpr int kLaneBytes = kInt4 ? 16 : KIND == kMxfp4 ? 128 : 32;
 };
 
-// One span of one weight row quarter: codes and, for the 4-bit formats, the
-// scale word (MXFP4: the E8M0 byte; INT4: bf16 scale << 16 | bf16 -(128+zero)).
-struct Frag {
-    u32x4 q;
-    uint32_t s;
+// Scales (and zeros) of one weight row for a block of U spans, as loaded.
+template <int KIND, int U>
+struct Scales {
+    static constexpr int kGroups = U * 128 / Format<KIND>::kGroup;
+    static constexpr int kWords = KIND == kBf16 ? 0 : (KIND == kMxfp4 ? kGroups : 2 * kGroups) / 4;
+    static constexpr int kZeroWords = KIND <= kMxfp4 ? 0 : (kGroups + 3) / 4;
+    uint32_t s[kWords > 0 ? kWords : 1];
+    uint32_t z[kZeroWords > 0 ? kZeroWords : 1];
 };
 
-// Per-lane addresses of a weight row.
-struct Row {
-    const uint8_t* data;       // + 16 * (lane / 16)
-    const uint8_t* scales;
-    const uint8_t* zeros;
-};
-
-template <int KIND>
-__device__ __forceinline__ Frag load_frag(const Row& r, int span, int c, int64_t last, int last_group)
+template <int WORDS>
+__device__ __forceinline__ void load_words(uint32_t* to, Buffer b, uint32_t lane_off, uint32_t off)
 {
-    Frag f;
-    // lanes past the row's end read its last 16 bytes instead (and zero them)
-    const int64_t off = min((int64_t)span * 64, last);
-    f.q = *reinterpret_cast<const u32x4*>(r.data + off);
-    f.s = 0;
-    if constexpr (KIND == kMxfp4) {
-        f.s = r.scales[min(span * 4 + c, last_group)];
-    } else if constexpr (Format<KIND>::kInt4) {
-        const int g = KIND == kInt4G32 ? span * 4 + c : KIND == kInt4G64 ? span * 2 + (c >> 1) : span;
-        const int gi = min(g, last_group);
-        const uint32_t sc = reinterpret_cast<const uint16_t*>(r.scales)[gi];
-        const uint32_t z = r.zeros ? r.zeros[gi] : 8u;
-        f.s = sc << 16 | 0xC300u | z;
+    if constexpr (WORDS >= 4) {
+        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_off, off, 0));
+        to[0] = v[0], to[1] = v[1], to[2] = v[2], to[3] = v[3];
+        if constexpr (WORDS == 8) load_words<4>(to + 4, b, lane_off, off + 16);
+    } else if constexpr (WORDS == 2) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, lane_off, off, 0));
+        to[0] = v[0], to[1] = v[1];
+    } else if constexpr (WORDS == 1) {
+        to[0] = __builtin_amdgcn_raw_buffer_load_b32(b, lane_off, off, 0);
     }
-    return f;
+}
+
+// INT4: the scale group, within a line, of a span's q-th run of parts.
+template <int KIND>
+constexpr int group_in_line(int v, int q)
+{
+    return KIND == kInt4G32 ? 2 * q + v : q;
+}
+
+// What one span of a weight row multiplies with, from its scale words.
+template <int KIND>
+struct SpanScale {
+    static constexpr int kGroups = Format<KIND>::kInt4 ? 4 / Format<KIND>::kGroupParts : 1;
+    float s[kGroups];          // MXFP4: this lane's group alone
+    uint32_t off[kGroups];     // INT4: bf16 -(128 + zero), twice
+};
+
+// Span v of the block's line ln.
+template <int KIND, int U>
+__device__ __forceinline__ SpanScale<KIND> span_scale(const Scales<KIND, U>& b, int ln, int v, int c, bool zeros)
+{
+    SpanScale<KIND> o;
+    if constexpr (KIND == kMxfp4) {
+        // byte 2c + v of the line's eight; the conversion takes the scale's
+        // exponent bits alone: byte 0 is 2^-127, byte 255 gives NaN
+        const uint64_t w = (uint64_t)b.s[2 * ln + 1] << 32 | b.s[2 * ln];
+        o.s[0] = __uint_as_float((uint32_t)(w >> (16 * c + 8 * v)) << 23);
+    } else if constexpr (Format<KIND>::kInt4) {
+#pragma unroll
+        for (int q = 0; q < SpanScale<KIND>::kGroups; ++q) {
+            const int i = ln * (256 / Format<KIND>::kGroup) + group_in_line<KIND>(v, q);
+            const uint32_t w = b.s[i / 2];
+            o.s[q] = __uint_as_float(i % 2 ? w & 0xFFFF0000u : w << 16);
+            o.off[q] = 0xC308C308u;
+            if (zeros)      // bytes zero, 0xC3, zero, 0xC3
+                o.off[q] = __builtin_amdgcn_perm(b.z[i / 4], 0xC3C3C3C3u,
+                                                 0x00040004u + (uint32_t)(i % 4) * 0x00010001u);
+        }
+    }
+    return o;
+}
+
+// Two loads of a line of 16 rows, each 8 rows of 128 bytes (lane: row l % 8,
+// bytes 16 * (l / 8)), to two operands of 16 rows (lane: row l % 16; q0 bytes
+// 32 * (l / 16), q1 the 16 behind): lanes 0-7 and 8-15 of a row of 16 trade.
+__device__ __forceinline__ void trade_halves(const u32x4& a, const u32x4& b, u32x4& q0, u32x4& q1)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // row_ror:8, written in lanes 8-15 (banks 2, 3) or 0-7 (banks 0, 1)
+        q0[i] = (uint32_t)__builtin_amdgcn_update_dpp((int)a[i], (int)b[i], 0x128, 0xF, 0xC, false);
+        q1[i] = (uint32_t)__builtin_amdgcn_update_dpp((int)b[i], (int)a[i], 0x128, 0xF, 0x3, false);
+    }
 }
 
 __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b)
@@ -124,34 +193,21 @@ __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b)
 
 // B operands of a span's instructions, from the loaded codes.
 template <int KIND>
-struct Operand {
-    u32x4 b[Format<KIND>::kParts];
-    uint32_t s[4 / Format<KIND>::kGroupParts];   // INT4: scale words of the span's groups
-};
-
-template <int KIND>
-__device__ __forceinline__ void expand(Frag f, bool empty, Operand<KIND>& o)
+__device__ __forceinline__ void expand(u32x4 f, const SpanScale<KIND>& s, u32x4 (&b)[Format<KIND>::kParts])
 {
-    if (empty) {      // columns past the end: 0 * 0
-        f.q = u32x4{0, 0, 0, 0};
-        f.s = KIND == kMxfp4 ? 127u : 0u;
-    }
     if constexpr (KIND == kBf16) {
-        o.b[0] = f.q;
+        b[0] = f;
     } else if constexpr (KIND == kMxfp4) {
-        // the conversion takes the scale's exponent bits alone, so byte 0 is
-        // 2^-127 and byte 255 gives NaN
-        const float sc = __uint_as_float(f.s << 23);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t w = f.q[j];
-            o.b[j][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0));
-            o.b[j][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1));
-            o.b[j][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2));
-            o.b[j][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3));
+            const uint32_t w = f[j];
+            b[j][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s.s[0], 0));
+            b[j][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s.s[0], 1));
+            b[j][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s.s[0], 2));
+            b[j][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s.s[0], 3));
         }
     } else {
-        uint32_t q[4] = {f.q[0], f.q[1], f.q[2], f.q[3]};
+        uint32_t q[4] = {f[0], f[1], f[2], f[3]};
         swap16(q[0], q[1]);
         swap16(q[2], q[3]);
         swap32(q[0], q[2]);
@@ -159,428 +215,773 @@ __device__ __forceinline__ void expand(Frag f, bool empty, Operand<KIND>& o)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o.b[j][i] = ((q[j] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-        if constexpr (KIND == kInt4G128) {
-            o.s[0] = f.s;
-        } else {
-            // lane c of a row holds group c's word (or c / 2's): all to all
-            uint32_t a = f.s, b = f.s;
-            if constexpr (KIND == kInt4G64) {
-                swap32(a, b);
-                o.s[0] = a;
-                o.s[1] = b;
-            } else {
-                swap16(a, b);
-                uint32_t a2 = a, b2 = b;
-                swap32(a, a2);
-                swap32(b, b2);
-                o.s[0] = a;
-                o.s[1] = b;
-                o.s[2] = a2;
-                o.s[3] = b2;
-            }
-        }
+            for (int i = 0; i < 4; ++i) b[j][i] = ((q[j] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
     }
 }
 
-// Adds one span's products to acc.  xa: the lane's A operand address of part
-// 0 in LDS; parts are kPartBytes apart.
+// Adds one span's products to acc.  x: the A operands of its parts, x_lo:
+// their second terms (LO).
 template <int KIND, bool LO>
-__device__ __forceinline__ void multiply(const Operand<KIND>& o, const unsigned char* xa,
-                                         int lo_bytes, f32x4& acc)
+__device__ __forceinline__ void multiply(const u32x4 (&b)[Format<KIND>::kParts],
+                                         const SpanScale<KIND>& s,
+                                         const u32x4 (&x)[(LO ? 2 : 1) * Format<KIND>::kParts],
+                                         f32x4& acc)
 {
     using F = Format<KIND>;
-    constexpr int kPartBytes = KIND == kMxfp4 ? 16 : 64;
     if constexpr (!F::kInt4) {
 #pragma unroll
         for (int j = 0; j < F::kParts; ++j) {
-            acc = mfma(*reinterpret_cast<const u32x4*>(xa + j * kPartBytes), o.b[j], acc);
-            if constexpr (LO)
-                acc = mfma(*reinterpret_cast<const u32x4*>(xa + lo_bytes + j * kPartBytes), o.b[j], acc);
+            acc = mfma(x[j], b[j], acc);
+            if constexpr (LO) acc = mfma(x[F::kParts + j], b[j], acc);
         }
     } else {
 #pragma unroll
-        for (int g = 0; g < 4 / F::kGroupParts; ++g) {
-            const uint32_t z = (o.s[g] & 0xFFFFu) * 0x10001u;
-            const u32x4 off = {z, z, z, z};
+        for (int g = 0; g < SpanScale<KIND>::kGroups; ++g) {
+            const u32x4 off = {s.off[g], s.off[g], s.off[g], s.off[g]};
             f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = g * F::kGroupParts; j < (g + 1) * F::kGroupParts; ++j) {
-                const u32x4 x = *reinterpret_cast<const u32x4*>(xa + j * kPartBytes);
-                sum = mfma(x, off, sum);
-                sum = mfma(x, o.b[j], sum);
+                sum = mfma(x[j], off, sum);
+                sum = mfma(x[j], b[j], sum);
                 if constexpr (LO) {
-                    const u32x4 xl = *reinterpret_cast<const u32x4*>(xa + lo_bytes + j * kPartBytes);
-                    sum = mfma(xl, off, sum);
-                    sum = mfma(xl, o.b[j], sum);
+                    sum = mfma(x[F::kParts + j], off, sum);
+                    sum = mfma(x[F::kParts + j], b[j], sum);
                 }
             }
-            const float sc = __uint_as_float(o.s[g] & 0xFFFF0000u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = fmaf(sc, sum[i], acc[i]);
+            for (int i = 0; i < 4; ++i) acc[i] = fmaf(s.s[g], sum[i], acc[i]);
         }
     }
 }
 
-// The i-th expert that has a row, and its rows.
-struct Group {
-    int expert;      // -1: there is none
-    int64_t row0;
-    int64_t rows;
+// Eight columns of x in the order in which INT4 codes come out of a word:
+// i and i + 4 side by side.
+__device__ __forceinline__ u32x4 pair_columns(u32x4 d)
+{
+    return u32x4{__builtin_amdgcn_perm(d[2], d[0], 0x05040100u),
+                 __builtin_amdgcn_perm(d[2], d[0], 0x07060302u),
+                 __builtin_amdgcn_perm(d[3], d[1], 0x05040100u),
+                 __builtin_amdgcn_perm(d[3], d[1], 0x07060302u)};
+}
+
+// ---- which rows belong to which expert --------------------------------------
+//
+// Each expert's rows are taken in passes of up to pass_rows; the tiles of all
+// passes form one sequence that is divided evenly over the blocks.
+
+constexpr int kPerLane = kMaxExperts / kWave;
+
+struct Groups {
+    int count[kMaxExperts];      // rows of each expert
+    int pass0[kWave];            // passes before lane l's 16 experts
+    int passes;                  // of all experts
 };
 
-// Bit e of the LDS bitmap is set where expert e has a row: finds the which-th.
-__device__ __forceinline__ int nth_expert(const uint32_t* bits, int which)
+// Rows of expert e, of which row0 is the first (received rows).
+__device__ __forceinline__ int received_rows(const ProductArgs& a, int e, int64_t* row0)
+{
+    int64_t n = a.count[e];
+    *row0 = a.psum[e];
+    if (a.cap > 0 && n > a.cap) n = a.cap;
+    if (*row0 + n > a.num_rows) n = *row0 < a.num_rows ? a.num_rows - *row0 : 0;
+    return (int)n;
+}
+
+// Passes that n rows take: ceil(n / pass_rows).
+__device__ __forceinline__ int passes_of(const ProductArgs& a, int n)
+{
+    const uint32_t up = (uint32_t)(n + a.pass_rows - 1);
+    return (int)(a.pass_magic ? __umulhi(up, a.pass_magic) : up);
+}
+
+// Counts the rows of every expert and numbers their passes.
+template <bool PAIRS, int kThreads>
+__device__ __forceinline__ void count_groups(const ProductArgs& a, Groups& g, uint16_t* ids)
+{
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    if constexpr (PAIRS) {
+        for (int e = tid; e < kMaxExperts; e += kThreads) g.count[e] = 0;
+        lds_barrier();
+        for (int p = tid; p < a.P; p += kThreads) {
+            const int e = a.topk[p];
+            const bool ok = (uint32_t)e < (uint32_t)a.E;
+            if (ok) atomicAdd(&g.count[e], 1);
+            else if (e != -1 && blockIdx.x == 0) atomicOr(a.flags, kFlagBadId);
+            ids[p] = ok ? (uint16_t)e : (uint16_t)0xFFFFu;
+        }
+    } else {
+        for (int e = tid; e < kMaxExperts; e += kThreads) {
+            int n = 0;
+            if (e < a.E) {
+                int64_t row0;
+                n = received_rows(a, e, &row0);
+                if (blockIdx.x == 0) {
+                    const int64_t all = a.cap > 0 && a.count[e] > a.cap ? a.cap : a.count[e];
+                    if (all > n) atomicOr(a.flags, kFlagCapacity);
+                }
+            }
+            g.count[e] = n;
+        }
+    }
+    lds_barrier();
+    if (tid < kWave) {
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+            mine += passes_of(a, g.count[lane * kPerLane + i]);
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+            const int v = __shfl_up(upto, d);
+            if (lane >= d) upto += v;
+        }
+        g.pass0[lane] = upto - mine;
+        if (lane == kWave - 1) g.passes = upto;
+    }
+    lds_barrier();
+}
+
+// Expert and first row (within it) of a pass.
+__device__ __forceinline__ void find_pass(const ProductArgs& a, const Groups& g, int pass, int* expert,
+                                          int* m0)
 {
     const int lane = threadIdx.x & (kWave - 1);
-    const uint32_t word = lane < kMaxExperts / 32 ? bits[lane] : 0u;
-    int upto = __popc(word);
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int v = __shfl_up(upto, d);
-        if (lane >= d) upto += v;
+    const uint64_t at = __ballot(g.pass0[lane] <= pass);
+    const int l = 63 - (int)__builtin_clzll(at);        // lane 0 always is
+    int left = pass - g.pass0[l];
+    int e = l * kPerLane;
+    for (;; ++e) {
+        const int n = passes_of(a, g.count[e]);
+        if (left < n || e == l * kPerLane + kPerLane - 1) break;
+        left -= n;
     }
-    const int before = upto - __popc(word);
-    const uint64_t here = __ballot(lane < kMaxExperts / 32 && before <= which && which < upto);
-    if (here == 0) return -1;
-    const int l = (int)__builtin_ctzll(here);
-    uint32_t w = (uint32_t)__builtin_amdgcn_readlane((int)word, l);
-    int n = which - __builtin_amdgcn_readlane(before, l);
-    while (n-- > 0) w &= w - 1;
-    return 32 * l + (int)__builtin_ctz(w);
+    *expert = __builtin_amdgcn_readfirstlane(e);
+    *m0 = __builtin_amdgcn_readfirstlane(left) * a.pass_rows;
 }
 
-// Pairs: the which-th chosen expert and its pairs, ascending, in list.
-__device__ __forceinline__ Group group_pairs(const ProductArgs& a, int which, uint32_t* bits,
-                                             int* wave_counts, uint16_t* list, bool report)
+// A handful of pairs (one a lane): every wave groups them by itself, without
+// LDS or a barrier; experts in the order of their first pairs.  e: the lane's
+// expert or -1.  Returns a mask of the lanes that are their expert's first.
+__device__ __forceinline__ uint64_t first_pairs(int e, int P)
 {
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    constexpr int kPer = kMaxPairs / kThreads;
-    if (tid < kMaxExperts / 32) bits[tid] = 0u;
-    lds_barrier();
-    // wave w holds the pairs [w*64*per, (w+1)*64*per) in order
-    const int per = (a.P + kThreads - 1) / kThreads;
-    int ids[kPer];
-    uint32_t bad = 0u;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if (i < per) {
-            const int p = (wave * per + i) * kWave + lane;
-            const int e = p < a.P ? a.topk[p] : -1;
-            const bool ok = (uint32_t)e < (uint32_t)a.E;
-            if (ok) atomicOr(&bits[e >> 5], 1u << (e & 31));
-            else if (e != -1) bad = kFlagBadId;
-            ids[i] = ok ? e : -1;
-        }
-    }
-    if (report && bad) atomicOr(a.flags, bad);
-    lds_barrier();
-    const int e = __builtin_amdgcn_readfirstlane(nth_expert(bits, which));
-    if (e < 0) return Group{-1, 0, 0};
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (i < per) mine += __popcll(__ballot(ids[i] == e));
-    if (lane == 0) wave_counts[wave] = mine;
-    lds_barrier();
-    int at = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) at += wave_counts[w];
-        total += wave_counts[w];
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if (i < per) {
-            const uint64_t m = __ballot(ids[i] == e);
-            if (ids[i] == e)
-                list[at + __popcll(m & ((1ull << lane) - 1))] =
-                    (uint16_t)((wave * per + i) * kWave + lane);
-            at += __popcll(m);
-        }
-    }
-    lds_barrier();
-    return Group{e, 0, total};
+    bool first = e >= 0;
+    for (int j = 0; j < P - 1; ++j)
+        first = first && !((int)(threadIdx.x & (kWave - 1)) > j && __builtin_amdgcn_readlane(e, j) == e);
+    return __ballot(first);
 }
 
-// Received rows: the which-th expert with a row.
-__device__ __forceinline__ Group group_received(const ProductArgs& a, int which, uint32_t* bits,
-                                                bool report)
+// The which-th expert and its pairs, given first_pairs.
+__device__ __forceinline__ void find_few(int e, uint64_t firsts, int which, int* expert, uint64_t* pairs)
 {
-    const int tid = threadIdx.x;
-    if (tid < kMaxExperts / 32) bits[tid] = 0u;
-    lds_barrier();
-    for (int e = tid; e < a.E; e += kThreads)
-        if (a.count[e] > 0) atomicOr(&bits[e >> 5], 1u << (e & 31));
-    lds_barrier();
-    const int e = __builtin_amdgcn_readfirstlane(nth_expert(bits, which));
-    if (e < 0) return Group{-1, 0, 0};
-    const int64_t row0 = a.psum[e];
-    int64_t n = a.count[e];
-    if (a.cap > 0 && n > a.cap) n = a.cap;
-    if (row0 + n > a.num_rows) {
-        if (report && tid == 0) atomicOr(a.flags, kFlagCapacity);
-        n = row0 < a.num_rows ? a.num_rows - row0 : 0;
-    }
-    return Group{e, row0, n};
+    const int lane = threadIdx.x & (kWave - 1);
+    const uint64_t at = __ballot((firsts >> lane & 1) && __popcll(firsts & ((1ull << lane) - 1)) == which);
+    *expert = __builtin_amdgcn_readlane(e, (int)__builtin_ctzll(at | 1ull << 63));
+    *pairs = __ballot(e == *expert);
 }
 
-// RT: 16-output tiles of a wave (with a gate: its gate tile and its up tile);
-// TT: 16-row tiles of x; U: spans in flight per wave and stage.
-template <int KIND, int EPI, int RT, int TT, int U>
-__global__ __launch_bounds__(kThreads) void k_product(ProductArgs a)
+// One wave: the pairs of an expert, ascending, from the m0-th on (up to most).
+__device__ __forceinline__ void list_pairs(const ProductArgs& a, const uint16_t* ids, int expert, int m0,
+                                           int most, int32_t* list)
 {
+    const int lane = threadIdx.x & (kWave - 1);
+    int at = -m0;
+    for (int p0 = 0; p0 < a.P && at < most; p0 += kWave) {
+        const int p = p0 + lane;
+        const bool hit = p < a.P && ids[p] == expert;
+        const uint64_t m = __ballot(hit);
+        const int to = at + __popcll(m & ((1ull << lane) - 1));
+        if (hit && to >= 0 && to < most) list[to] = p;
+        at += __popcll(m);
+    }
+}
+
+// ---- the kernel ------------------------------------------------------------------
+
+constexpr int kSegments = 8;        // passes whose x is in LDS at a time
+constexpr int kListRows = 128;      // ... and their rows, at most
+
+// A block takes an even share of the tiles and walks it a batch at a time: the
+// tiles of as many passes ("segments") as have their rows in LDS together.
+// Its kWaves waves form kWaves / kw teams; a team takes every (kWaves / kw)-th
+// tile of the batch, and its kw waves every kw-th block of kU spans of the
+// tile's columns.  RT = 2: 16-output tiles of a wave (with a gate: its gate
+// tile and its up tile); TT: 16-row tiles of x.
+// DIRECT: x is read from memory, a block ahead, not through LDS.
+template <int KIND, int EPI, int TT, bool DIRECT, int kU, int kWaves>
+__global__ __launch_bounds__(kWaves* kWave, kWaves == 4 ? (KIND <= kMxfp4 ? 3 : 2) : kWaves / 4) void k_product(ProductArgs a)
+{
+    constexpr int kThreads = kWaves * kWave;
     using F = Format<KIND>;
+    constexpr int RT = 2;
+    constexpr int kL = kU / 2;                           // lines of a block
     constexpr bool kGate = EPI == kSwigluBf16 || EPI == kSwigluSplit;
     constexpr bool kPairs = EPI == kSwigluSplit || EPI == kStoreF32;
     constexpr bool LO = EPI == kStoreF32;
     constexpr int kPlanes = LO ? 2 : 1;
-    constexpr int kTileUnits = kGate ? 16 : 16 * RT;     // outputs of a wave
-    static_assert(!kGate || RT == 2, "a gated wave holds a gate tile and an up tile");
+    constexpr int kParts = F::kParts;
+    constexpr int kTileUnits = kGate ? 16 : 32;          // outputs of a tile
+    static_assert(!DIRECT || TT == 1, "x from memory: one row tile");
+    constexpr int kScaleBytes = F::kInt4 ? 2 : 1;
 
-    extern __shared__ __align__(16) unsigned char smem[];   // x, later the waves' sums
-    __shared__ uint32_t bits[kMaxExperts / 32];
-    __shared__ int wave_counts[kWaves];
-    __shared__ uint16_t list[kPairs ? kMaxPairs : 1];
+    extern __shared__ __align__(16) unsigned char smem[];   // x, then the waves' sums
+    __shared__ Groups groups;
+    __shared__ uint16_t ids[kPairs ? kMaxPairs : 1];
+    __shared__ int32_t list[kListRows];                  // rows of x in LDS: their output rows
+    __shared__ int seg_expert[kSegments], seg_rows[kSegments], seg_first[kSegments];
+    f32x4* const red = reinterpret_cast<f32x4*>(smem + a.x_bytes);
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int n = lane & 15, c = lane >> 4;
     const int kw = a.kw, rw = kWaves / kw;
     const int kq = wave % kw, rg = wave / kw;
+    const bool grouped = kPairs || a.count != nullptr;
 
-    const bool first_tile = blockIdx.x == 0;
-    Group g;
-    if constexpr (kPairs) g = group_pairs(a, blockIdx.y, bits, wave_counts, list, first_tile && blockIdx.y == 0);
-    else if (a.count) g = group_received(a, blockIdx.y, bits, first_tile);
-    else g = Group{0, 0, a.num_rows};
-    if (g.expert < 0) return;
-
-    // ---- this wave's weight rows
-    const int unit0 = (blockIdx.x * rw + rg) * kTileUnits;
-    const int64_t expert_rows = (int64_t)g.expert * a.w.rows;
-    Row row[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int u = min(unit0 + (kGate ? 0 : 16 * r) + n, a.units - 1);
-        const int64_t at = expert_rows + (kGate && r == 1 ? a.units + u : u);
-        row[r].data = a.w.data + at * a.w.row_bytes + 16 * c;
-        row[r].scales = a.w.scales + at * a.w.row_groups * (F::kInt4 ? 2 : 1);
-        row[r].zeros = a.w.zeros ? a.w.zeros + at * a.w.row_groups : nullptr;
+    int passes;
+    const bool few = kPairs && a.P <= kWave && a.P <= a.pass_rows;
+    int my_expert = -1;      // few: of pair `lane`
+    uint64_t firsts = 0;
+    if (few) {
+        if (lane < a.P) my_expert = a.topk[lane];
+        if ((uint32_t)my_expert >= (uint32_t)a.E) {
+            if (my_expert != -1 && blockIdx.x == 0) atomicOr(a.flags, kFlagBadId);
+            my_expert = -1;
+        }
+        firsts = first_pairs(my_expert, a.P);
+        passes = __popcll(firsts);
+    } else if (grouped) {
+        count_groups<kPairs, kThreads>(a, groups, ids);
+        passes = groups.passes;
+    } else {
+        passes = a.dense_passes;
     }
-    const int64_t last = a.w.row_bytes - 16 - 16 * c;
-    const int last_group = (int)a.w.row_groups - 1;
-    const int spans = (int)((a.w.row_bytes + 63) / 64);
-    const int iters = (spans + kw - 1) / kw;
-    const bool tail_lane = (int64_t)(spans - 1) * 64 + 16 * c >= a.w.row_bytes;
+    const int tiles = (a.units + kTileUnits - 1) / kTileUnits;
+    // this block's share [at, stop) of all tiles (fewer than 2^31)
+    const uint32_t all = (uint32_t)passes * (uint32_t)tiles;
+    const uint32_t share = all / gridDim.x, more = all - share * gridDim.x;
+    uint32_t at = blockIdx.x * share + min(blockIdx.x, more);
+    const uint32_t stop = at + share + (blockIdx.x < more ? 1u : 0u);
 
-    const int64_t block_step = (kPairs || a.count) ? 16 * TT : 16 * TT * (int64_t)gridDim.y;
-    const int64_t block0 = (kPairs || a.count) ? 0 : 16 * TT * (int64_t)blockIdx.y;
-    for (int64_t m0 = block0; m0 < g.rows; m0 += block_step) {
-        const int rows = (int)min(g.rows - m0, (int64_t)(16 * TT));
-        // iterations whose columns of these rows fit LDS at once
-        int chunk = (a.x_bytes / (rows * kPlanes) - 16) / (kw * F::kSpan * 2);
-        chunk = min(chunk, iters);
-        const int chunk_cols = chunk * kw * F::kSpan;
-        const int stride = chunk_cols * 2 + 16;      // 16: rows start in different banks
-        const int lo_bytes = rows * stride;
+    const int row_bytes = (int)a.w.row_bytes, row_groups = (int)a.w.row_groups;
+    const bool has_zeros = F::kInt4 && a.w.zeros != nullptr;
+    const int full = row_bytes / 128;                // whole lines
+    const bool tail = row_bytes % 128 != 0;          // columns behind them
+    const int blocks = (full + kL - 1) / kL;
+    const int mine = (blocks - kq + kw - 1) / kw;    // blocks of this wave per tile
+    // lines whose scales are loaded a block at a time, as whole words
+    const int quick = row_groups % 4 == 0 ? full : 0;
+    const int cols_up = (a.w.cols + F::kLine - 1) / F::kLine * F::kLine;
+    const int stride = cols_up * 2 + 16;             // of x in LDS; 16: rows start in different banks
 
-        f32x4 acc[RT][TT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    while (at < stop) {
+        // ---- a batch: tiles [at, batch_stop) of passes pass0, pass0 + 1, ...
+        const int pass0 = (int)(at / (uint32_t)tiles);
+        int segments = 0, lds_rows = 0;
+        for (int pass = pass0; segments < kSegments && (uint32_t)pass * (uint32_t)tiles < stop; ++pass) {
+            int expert = 0, m0 = 0, rows;
+            int64_t row0 = 0;
+            uint64_t pairs = 0;
+            if (few) {
+                find_few(my_expert, firsts, pass, &expert, &pairs);
+                rows = (int)__popcll(pairs);
+            } else if (grouped) {
+                find_pass(a, groups, pass, &expert, &m0);
+                rows = min(groups.count[expert] - m0, a.pass_rows);
+                if constexpr (!kPairs) row0 = (int64_t)a.psum[expert] + m0;
+            } else {
+                row0 = (int64_t)pass * a.pass_rows;
+                rows = (int)min(a.num_rows - row0, (int64_t)a.pass_rows);
+            }
+            rows = __builtin_amdgcn_readfirstlane(rows);
+            if (segments > 0 && lds_rows + rows > a.x_rows) break;
+            // every wave writes the same values, but for long lists of pairs
+            if (few) {
+                if (pairs >> lane & 1) list[lds_rows + __popcll(pairs & ((1ull << lane) - 1))] = lane;
+            } else if constexpr (kPairs) {
+                if (wave == segments % kWaves) list_pairs(a, ids, expert, m0, rows, list + lds_rows);
+            } else {
+                if (lane < rows) list[lds_rows + lane] = (int32_t)(row0 + lane);
+            }
+            if (lane == 0) {
+                seg_expert[segments] = expert;
+                seg_rows[segments] = rows;
+                seg_first[segments] = lds_rows;
+            }
+            lds_rows += rows;
+            ++segments;
+        }
+        const uint32_t batch_stop = min(stop, (uint32_t)(pass0 + segments) * (uint32_t)tiles);
+        if (kPairs && !few) lds_barrier();
 
-        Frag f[U][RT];
+        // ---- loads: where the next block comes from
+        Buffer data[RT], scales[RT], zeros[RT];
+        uint32_t data_off[RT][2], scale_off[RT], zero_off[RT];
+        // of a tile of the batch: its segment, its first output
+        auto segment_of = [&](uint32_t t) { return (int)(t / (uint32_t)tiles) - pass0; };
+        auto unit_of = [&](uint32_t t, int seg) { return (int)(t - (uint32_t)(pass0 + seg) * (uint32_t)tiles) * kTileUnits; };
+        auto aim = [&](uint32_t t) {      // past the batch: at nothing
+            const bool there = t < batch_stop && mine > 0;
+            if (!there) t = at;
+            const int seg = segment_of(t), unit0 = unit_of(t, seg);
+            const int64_t expert_row = (int64_t)__builtin_amdgcn_readfirstlane(seg_expert[seg]) * a.w.rows;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int r = 0; r < RT; ++r) {
+                // idle lanes repeat the last output
+                const int t0 = min(unit0 + (kGate ? 0 : 16 * r), a.units - 1);
+                const int have = min(16, a.units - t0);
+                const int64_t first = expert_row + (kGate && r == 1 ? a.units : 0) + t0;
+                data[r] = make_buffer(a.w.data + first * row_bytes, there ? (int64_t)have * row_bytes : 0);
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-                f[u][r] = load_frag<KIND>(row[r], min(u * kw + kq, spans - 1), c, last, last_group);
-
-        for (int i0 = 0; i0 < iters; i0 += chunk) {
-            // ---- x to LDS: columns [i0 * kw * span, + chunk_cols) of every row
-            lds_barrier();
-            const int col0 = i0 * kw * F::kSpan;
-            const int vecs = chunk_cols / 8;
-            for (int v = tid; v < rows * vecs; v += kThreads) {
-                const int m = v / vecs, k = (v - m * vecs) * 8;
-                int64_t xr;
-                if constexpr (kPairs) {
-                    const int p = list[m0 + m];
-                    xr = a.x_per_pair ? p : p / a.K;
-                } else {
-                    xr = g.row0 + m0 + m;
+                for (int v = 0; v < 2; ++v)
+                    data_off[r][v] = (uint32_t)min(8 * v + (lane & 7), have - 1) * (uint32_t)row_bytes +
+                                     16u * (lane >> 3);
+                if constexpr (KIND != kBf16) {
+                    scales[r] = make_buffer(a.w.scales + first * row_groups * kScaleBytes,
+                                            there ? (int64_t)have * row_groups * kScaleBytes : 0);
+                    scale_off[r] = (uint32_t)min(n, have - 1) * (uint32_t)(row_groups * kScaleBytes);
                 }
-                const bool in = col0 + k < a.w.cols;
-                const int64_t at = xr * a.ldx + col0 + k;
-#pragma unroll
-                for (int pl = 0; pl < kPlanes; ++pl) {
-                    u32x4 d = {0, 0, 0, 0};
-                    if (in) d = *reinterpret_cast<const u32x4*>((pl ? a.x_lo : a.x) + at);
-                    if constexpr (F::kInt4)     // columns i and i+4 side by side, as the codes come out
-                        d = u32x4{__builtin_amdgcn_perm(d[2], d[0], 0x05040100u),
-                                  __builtin_amdgcn_perm(d[2], d[0], 0x07060302u),
-                                  __builtin_amdgcn_perm(d[3], d[1], 0x05040100u),
-                                  __builtin_amdgcn_perm(d[3], d[1], 0x07060302u)};
-                    *reinterpret_cast<u32x4*>(smem + pl * lo_bytes + m * stride + 2 * k) = d;
+                if constexpr (F::kInt4) {
+                    zeros[r] = make_buffer(a.w.zeros + first * row_groups, there ? (int64_t)have * row_groups : 0);
+                    zero_off[r] = (uint32_t)min(n, have - 1) * (uint32_t)row_groups;
                 }
             }
-            lds_barrier();
-
-            // ---- this wave's spans of the chunk
-            const int end = min(i0 + chunk, iters);
-            const unsigned char* xa[TT];
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const int m = 16 * t + n < rows ? 16 * t + n : 0;     // others: any row
-                xa[t] = smem + m * stride + (KIND == kMxfp4 ? 64 : 16) * c;
-            }
-            for (int i = i0; i < end; i += U) {
-                const int next = i + U < end ? i + U : end;
-                Frag fn[U][RT];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        fn[u][r] = load_frag<KIND>(row[r], min((next + u) * kw + kq, spans - 1), c,
-                                                   last, last_group);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int span = (i + u) * kw + kq;
-                    if (i + u < end && span < spans) {
-                        const bool empty = span == spans - 1 && tail_lane;
-#pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            Operand<KIND> o;
-                            expand<KIND>(f[u][r], empty, o);
-#pragma unroll
-                            for (int t = 0; t < TT; ++t)
-                                if (t == 0 || 16 * t < rows)
-                                    multiply<KIND, LO>(o, xa[t] + (span - i0 * kw) * F::kSpan * 2,
-                                                       lo_bytes, acc[r][t]);
-                        }
-                    }
+        };
+        auto load_half = [&](int r, int v, int line) {
+            return load_weights(data[r], data_off[r][v], (uint32_t)line * 128u);
+        };
+        auto load_scales = [&](int r, int block, Scales<KIND, kU>& o) {
+            constexpr uint32_t kG = Scales<KIND, kU>::kGroups;
+            if constexpr (KIND != kBf16)
+                load_words<Scales<KIND, kU>::kWords>(o.s, scales[r], scale_off[r], block * kG * kScaleBytes);
+            if constexpr (F::kInt4) {
+                if (has_zeros) {
+                    if constexpr (kG == 2)
+                        o.z[0] = __builtin_amdgcn_raw_buffer_load_b16(zeros[r], zero_off[r], block * kG, 0);
+                    else
+                        load_words<Scales<KIND, kU>::kZeroWords>(o.z, zeros[r], zero_off[r], block * kG);
                 }
+            }
+        };
+
+        // one block of weights ahead: a line's registers are loaded again as
+        // soon as they are used
+        u32x4 f[kU][RT];
+        Scales<KIND, kU> next[RT];
+        aim(at + rg);
+        {
+            const int l0 = at + rg < batch_stop && mine > 0 ? kq * kL : 0;
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+            for (int r = 0; r < RT; ++r) {
+                if (l0 + kL <= quick) load_scales(r, l0 / kL, next[r]);
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) f[u][r] = fn[u][r];
+                for (int u = 0; u < kU; ++u) f[u][r] = load_half(r, u % 2, max(min(l0 + u / 2, full - 1), 0));
             }
         }
 
-        // ---- the waves' shares of a sum, added in wave order
-        if (kw > 1) {
-            lds_barrier();
-            f32x4* red = reinterpret_cast<f32x4*>(smem);
-            if (kq > 0)
+        // ---- x to LDS
+        auto x_row = [&](int m) -> int64_t {
+            const int row = list[m];
+            if constexpr (kPairs) return a.x_per_pair ? row : row / a.K;
+            else return row;
+        };
+        const int lo_bytes = a.x_rows * stride;
+        if constexpr (!DIRECT) {
+            const int vecs = cols_up / 8;
+            for (int m = wave; m < lds_rows; m += kWaves) {
+                const uint16_t* from = a.x + x_row(m) * a.ldx;
+                const uint16_t* from_lo = LO ? a.x_lo + x_row(m) * a.ldx : nullptr;
+#pragma unroll 4
+                for (int v = lane; v < vecs; v += kWave)
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
+                    for (int pl = 0; pl < kPlanes; ++pl) {
+                        u32x4 d = {0, 0, 0, 0};
+                        if (v * 8 < a.w.cols) d = *reinterpret_cast<const u32x4*>((pl ? from_lo : from) + v * 8);
+                        if constexpr (F::kInt4) d = pair_columns(d);
+                        *reinterpret_cast<u32x4*>(smem + pl * lo_bytes + m * stride + 16 * v) = d;
+                    }
+            }
+            lds_barrier();
+        }
+
+        const int64_t lo_elems = LO ? a.x_lo - a.x : 0;
+        int seg = -1, rows = 0, first_row = 0;
+        int64_t expert_row = 0;
+        const uint16_t* xg = nullptr;      // this lane's row of x, in memory
+        const unsigned char* xa[TT];       // ... in LDS
+        auto enter = [&](int to) {
+            seg = to;
+            rows = __builtin_amdgcn_readfirstlane(seg_rows[to]);
+            first_row = __builtin_amdgcn_readfirstlane(seg_first[to]);
+            expert_row = (int64_t)__builtin_amdgcn_readfirstlane(seg_expert[to]) * a.w.rows;
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const int m = first_row + (16 * t + n < rows ? 16 * t + n : 0);     // others: any row
+                xa[t] = smem + m * stride + c * F::kLaneBytes;
+                if constexpr (DIRECT) xg = a.x + x_row(m) * a.ldx + c * (F::kLaneBytes / 2);
+            }
+        };
+        // A operands of span v of a line, for row tile t: from LDS, or from
+        // memory (of a last, partial line with zeros past the end)
+        auto x_lds = [&](int t, int line, int v, u32x4 (&x)[kPlanes * kParts]) {
+            const unsigned char* p = xa[t] + line * F::kLineBytes + v * F::kSpanBytes;
+#pragma unroll
+            for (int pl = 0; pl < kPlanes; ++pl)
+#pragma unroll
+                for (int j = 0; j < kParts; ++j)
+                    x[pl * kParts + j] = *reinterpret_cast<const u32x4*>(p + pl * lo_bytes + j * F::kPartBytes);
+        };
+        auto x_memory = [&](int line, int v, bool partial, u32x4 (&x)[kPlanes * kParts]) {
+            const uint16_t* p = xg + (int64_t)line * F::kLine + v * (F::kSpanBytes / 2);
+#pragma unroll
+            for (int pl = 0; pl < kPlanes; ++pl)
+#pragma unroll
+                for (int j = 0; j < kParts; ++j) {
+                    const int k = j * (F::kPartBytes / 2);
+                    if (partial && line * F::kLine + v * (F::kSpanBytes / 2) + k + c * (F::kLaneBytes / 2) >= a.w.cols)
+                        x[pl * kParts + j] = u32x4{0, 0, 0, 0};
+                    else
+                        x[pl * kParts + j] = *reinterpret_cast<const u32x4*>(p + pl * lo_elems + k);
+                }
+        };
+        // scales of a single span: groups past the row's end read the last one
+        auto load_span_scale = [&](int unit0, int r, int line, int v) {
+            SpanScale<KIND> o;
+            const int u = min(unit0 + (kGate ? 0 : 16 * r) + n, a.units - 1);
+            const int64_t base = (expert_row + (kGate && r == 1 ? a.units : 0) + u) * row_groups;
+            if constexpr (KIND == kMxfp4) {
+                const int gi = min(line * 8 + 2 * c + v, row_groups - 1);
+                o.s[0] = __uint_as_float((uint32_t)a.w.scales[base + gi] << 23);
+            } else if constexpr (F::kInt4) {
+#pragma unroll
+                for (int q = 0; q < SpanScale<KIND>::kGroups; ++q) {
+                    const int want = line * (256 / F::kGroup) + group_in_line<KIND>(v, q);
+                    const int gi = min(want, row_groups - 1);
+                    const uint32_t w = reinterpret_cast<const uint16_t*>(a.w.scales)[base + gi];
+                    o.s[q] = want == gi ? __uint_as_float(w << 16) : 0.f;
+                    o.off[q] = (0xC300u | (has_zeros ? a.w.zeros[base + gi] : 8u)) * 0x10001u;
+                }
+            }
+            return o;
+        };
+
+        u32x4 xr[DIRECT ? kU : 1][kPlanes * kParts];
+        if (at + rg < batch_stop) enter(segment_of(at + rg));
+        if constexpr (DIRECT) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (full > 0 && seg >= 0) x_memory(min(kq * kL + u / 2, full - 1), u % 2, false, xr[u]);
+        }
+        const int steps = (int)((batch_stop - at + rw - 1) / rw);
+        for (int step = 0; step < steps; ++step) {
+            const uint32_t tile = at + step * rw + rg;
+            const bool here = tile < batch_stop;
+            f32x4 acc[RT][TT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            int unit0 = 0;
+            // A operands of a span; x0: the ones that were loaded ahead, if any
+            auto x_of = [&](int t, int line, int v, bool partial, u32x4 (*x0)[kPlanes * kParts],
+                            u32x4 (&x)[kPlanes * kParts]) {
+                if constexpr (!DIRECT) {
+                    x_lds(t, line, v, x);
+                } else if (x0 != nullptr) {
+#pragma unroll
+                    for (int i = 0; i < kPlanes * kParts; ++i) x[i] = (*x0)[i];
+                } else {
+                    x_memory(line, v, partial, x);
+                }
+                if constexpr (DIRECT && F::kInt4)
+#pragma unroll
+                    for (int i = 0; i < kPlanes * kParts; ++i) x[i] = pair_columns(x[i]);
+            };
+            // adds a span
+            auto use = [&](const u32x4 (&q)[RT], const SpanScale<KIND> (&s)[RT], int line, int v, bool partial,
+                           u32x4 (*x0)[kPlanes * kParts]) {
+                if constexpr (TT == 1) {
+                    u32x4 x[kPlanes * kParts];
+                    x_of(0, line, v, partial, x0, x);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        u32x4 b[kParts];
+                        expand<KIND>(q[r], s[r], b);
+                        multiply<KIND, LO>(b, s[r], x, acc[r][0]);
+                    }
+                } else {
+                    u32x4 b[RT][kParts];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) expand<KIND>(q[r], s[r], b[r]);
 #pragma unroll
                     for (int t = 0; t < TT; ++t)
-                        red[((wave * RT + r) * TT + t) * kWave + lane] = acc[r][t];
-            lds_barrier();
-            if (kq == 0)
-                for (int q = 1; q < kw; ++q)
+                        if (t == 0 || 16 * t < rows) {
+                            u32x4 x[kPlanes * kParts];
+                            x_of(t, line, v, partial, x0, x);
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) multiply<KIND, LO>(b[r], s[r], x, acc[r][t]);
+                        }
+                }
+            };
+
+            if (here) {
+                const int to = segment_of(tile);
+                if (to != seg) {
+                    enter(to);
+                    // x of the first block of another pass's tile
+                    if constexpr (DIRECT) {
+#pragma unroll
+                        for (int u = 0; u < kU; ++u)
+                            if (full > 0) x_memory(min(kq * kL + u / 2, full - 1), u % 2, false, xr[u]);
+                    }
+                }
+                unit0 = unit_of(tile, seg);
+                for (int j = 0; j < mine; ++j) {
+                    const int line0 = (kq + j * kw) * kL;
+                    // the block after this one: of this tile, of the next, or none
+                    int next0 = line0 + kw * kL;
+                    if (j + 1 == mine) {
+                        aim(tile + rw);
+                        next0 = tile + rw < batch_stop ? kq * kL : 0;
+                    }
+                    // both spans of line ln: codes from load order to row
+                    // order, the registers loaded again, then the products
+                    auto take = [&](int ln, u32x4 (&q0)[RT], u32x4 (&q1)[RT]) {
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            trade_halves(f[2 * ln][r], f[2 * ln + 1][r], q0[r], q1[r]);
+                            f[2 * ln][r] = load_half(r, 0, min(next0 + ln, full - 1));
+                            f[2 * ln + 1][r] = load_half(r, 1, min(next0 + ln, full - 1));
+                        }
+                    };
+                    auto refill_x = [&](int ln) {
+                        if constexpr (DIRECT) {
+                            x_memory(min(next0 + ln, full - 1), 0, false, xr[2 * ln]);
+                            x_memory(min(next0 + ln, full - 1), 1, false, xr[2 * ln + 1]);
+                        }
+                    };
+                    if (line0 + kL <= quick) {
+                        Scales<KIND, kU> cur[RT];
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            cur[r] = next[r];
+                            if (next0 + kL <= quick) load_scales(r, next0 / kL, next[r]);
+                        }
+#pragma unroll
+                        for (int ln = 0; ln < kL; ++ln) {
+                            u32x4 q0[RT], q1[RT];
+                            SpanScale<KIND> s[RT];
+                            take(ln, q0, q1);
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) s[r] = span_scale<KIND, kU>(cur[r], ln, 0, c, has_zeros);
+                            use(q0, s, line0 + ln, 0, false, &xr[DIRECT ? 2 * ln : 0]);
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) s[r] = span_scale<KIND, kU>(cur[r], ln, 1, c, has_zeros);
+                            use(q1, s, line0 + ln, 1, false, &xr[DIRECT ? 2 * ln + 1 : 0]);
+                            refill_x(ln);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    } else {
+                        // the row's last, partial block, or odd scale rows
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+                            if (next0 + kL <= quick) load_scales(r, next0 / kL, next[r]);
+#pragma unroll
+                        for (int ln = 0; ln < kL; ++ln) {
+                            u32x4 q0[RT], q1[RT];
+                            take(ln, q0, q1);
+                            if (line0 + ln < full) {
+                                SpanScale<KIND> s[RT];
+#pragma unroll
+                                for (int r = 0; r < RT; ++r) s[r] = load_span_scale(unit0, r, line0 + ln, 0);
+                                use(q0, s, line0 + ln, 0, false, &xr[DIRECT ? 2 * ln : 0]);
+#pragma unroll
+                                for (int r = 0; r < RT; ++r) s[r] = load_span_scale(unit0, r, line0 + ln, 1);
+                                use(q1, s, line0 + ln, 1, false, &xr[DIRECT ? 2 * ln + 1 : 0]);
+                            }
+                            refill_x(ln);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                }
+                // columns behind the last whole line: the team's first wave,
+                // with zeros in the lanes past the end
+                if (tail && kq == 0) {
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        u32x4 q[RT];
+                        SpanScale<KIND> s[RT];
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            const int u = min(unit0 + (kGate ? 0 : 16 * r) + n, a.units - 1);
+                            const int64_t row = expert_row + (kGate && r == 1 ? a.units : 0) + u;
+                            const int byte = full * 128 + 16 * (2 * c + v);
+                            q[r] = u32x4{0, 0, 0, 0};
+                            if (byte < row_bytes)
+                                q[r] = *reinterpret_cast<const u32x4*>(a.w.data + row * row_bytes + byte);
+                            s[r] = load_span_scale(unit0, r, full, v);
+                            if (KIND == kMxfp4 && byte >= row_bytes) s[r].s[0] = 1.f;
+                        }
+                        use(q, s, full, v, true, nullptr);
+                    }
+                }
+            }
+
+            // ---- the waves' shares of a sum, added in wave order
+            if (kw > 1) {
+                f32x4* const mine_red = red + (step & 1) * kWaves * RT * TT * kWave;
+                if (kq > 0)
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
 #pragma unroll
                         for (int t = 0; t < TT; ++t)
-                            acc[r][t] += red[(((wave + q) * RT + r) * TT + t) * kWave + lane];
-        }
+                            mine_red[((wave * RT + r) * TT + t) * kWave + lane] = acc[r][t];
+                lds_barrier();
+                if (kq == 0)
+                    for (int q = 1; q < kw; ++q)
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+#pragma unroll
+                            for (int t = 0; t < TT; ++t)
+                                acc[r][t] += mine_red[(((wave + q) * RT + r) * TT + t) * kWave + lane];
+            }
 
-        // ---- store: this lane has output n of rows 4c .. 4c+3 of each tile
-        if (kq == 0) {
+            // ---- store: this lane has output n of rows 4c .. 4c+3 of each tile
+            if (kq == 0 && here) {
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
+                for (int t = 0; t < TT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int m = 16 * t + 4 * c + i;
-                    if (m >= rows) continue;
-                    int64_t yr;
-                    if constexpr (kPairs) yr = list[m0 + m];
-                    else yr = g.row0 + m0 + m;
-                    if constexpr (kGate) {
-                        const int u = unit0 + n;
-                        if (u >= a.units) continue;
-                        const float ga = acc[0][t][i];
-                        const float v = ga / (1.f + __expf(-ga)) * acc[1][t][i];
-                        const int64_t at = yr * a.ldy + u;
-                        if constexpr (EPI == kSwigluBf16) {
-                            reinterpret_cast<uint16_t*>(a.y)[at] = to_bf16(v);
-                        } else {
-                            // two bf16 terms hold 16 bits of the fp32 value (an
-                            // infinity or NaN stays in the first)
-                            const float wv = a.weights ? a.weights[yr] * v : v;
-                            const uint16_t hi = to_bf16(wv);
-                            reinterpret_cast<uint16_t*>(a.y)[at] = hi;
-                            a.y_lo[at] = (hi & 0x7F80u) == 0x7F80u ? (uint16_t)0
-                                                                   : to_bf16(wv - from_bf16(hi));
-                        }
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            const int u = unit0 + 16 * r + n;
+                    for (int i = 0; i < 4; ++i) {
+                        const int m = 16 * t + 4 * c + i;
+                        if (m >= rows) continue;
+                        const int64_t yr = list[first_row + m];
+                        if constexpr (kGate) {
+                            const int u = unit0 + n;
                             if (u >= a.units) continue;
-                            const int64_t at = yr * a.ldy + u;
-                            if constexpr (EPI == kStoreBf16)
-                                reinterpret_cast<uint16_t*>(a.y)[at] = to_bf16(acc[r][t][i]);
-                            else
-                                reinterpret_cast<float*>(a.y)[at] = acc[r][t][i];
+                            const float ga = acc[0][t][i];
+                            const float v = ga / (1.f + __expf(-ga)) * acc[1][t][i];
+                            const int64_t to = yr * a.ldy + u;
+                            if constexpr (EPI == kSwigluBf16) {
+                                reinterpret_cast<uint16_t*>(a.y)[to] = to_bf16(v);
+                            } else {
+                                // two bf16 terms hold 16 bits of the fp32 value
+                                // (an infinity or NaN stays in the first)
+                                const float wv = a.weights ? a.weights[yr] * v : v;
+                                const uint16_t hi = to_bf16(wv);
+                                reinterpret_cast<uint16_t*>(a.y)[to] = hi;
+                                a.y_lo[to] = (hi & 0x7F80u) == 0x7F80u ? (uint16_t)0
+                                                                       : to_bf16(wv - from_bf16(hi));
+                            }
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) {
+                                const int u = unit0 + 16 * r + n;
+                                if (u >= a.units) continue;
+                                const int64_t to = yr * a.ldy + u;
+                                if constexpr (EPI == kStoreBf16)
+                                    reinterpret_cast<uint16_t*>(a.y)[to] = to_bf16(acc[r][t][i]);
+                                else
+                                    reinterpret_cast<float*>(a.y)[to] = acc[r][t][i];
+                            }
                         }
                     }
-                }
+            }
         }
+        at = batch_stop;
+        if (at < stop) lds_barrier();      // x and the list are read; the next batch's follow
     }
 }
 
 // ---- launch -------------------------------------------------------------
 
-template <int KIND, int EPI, int RT, int TT, int U>
-hipError_t launch_shape(ProductArgs a, int slots, int64_t max_rows, hipStream_t s)
+inline int num_cus()
+{
+    static const int n = [] {
+        int dev = 0, v = 0;
+        if (hipGetDevice(&dev) != hipSuccess ||
+            hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v < 1)
+            v = 256;
+        return v;
+    }();
+    return n;
+}
+
+// Dynamic LDS of a block, at most (its static arrays take 13 KB of the CU's
+// 160 KB).
+constexpr int64_t kLdsRoom = 131072;
+
+// LDS in which the waves of a team add their sums: two buffers.
+constexpr int64_t sums_bytes(int waves, int kw, int tt)
+{
+    return kw > 1 ? 2 * (int64_t)waves * 2 * tt * kWave * 16 : 0;
+}
+
+template <int KIND, int EPI, int TT, bool DIRECT, int U, int kWaves>
+hipError_t launch_shape(ProductArgs a, int64_t room, int kw, int64_t rows, int64_t max_rows, int64_t tiles,
+                        hipStream_t s)
 {
     using F = Format<KIND>;
     constexpr int kPlanes = EPI == kStoreF32 ? 2 : 1;
-    constexpr bool kGate = EPI == kSwigluBf16 || EPI == kSwigluSplit;
-    const int kw = kWaves;
-    const int rows = (int)(max_rows < 16 * TT ? max_rows : 16 * TT);
-    const int64_t step = (int64_t)kw * F::kSpan * 2;
-    const int64_t need = rows * kPlanes * (step + 16);
-    const int64_t whole = rows * kPlanes * ((a.w.cols * 2 + step - 1) / step * step + 16);
-    int64_t bytes = 32768;
-    bytes = bytes < whole ? bytes : whole;
-    bytes = bytes > need ? bytes : need;
-    const int64_t red = (int64_t)kWaves * RT * TT * kWave * 16;
-    bytes = bytes > red ? bytes : red;
     a.kw = kw;
-    a.x_bytes = (int)bytes;
-    const int per_block = (kWaves / kw) * (kGate ? 16 : 16 * RT);
-    const dim3 grid((a.units + per_block - 1) / per_block, slots);
-    if (bytes > 65536)
-        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_product<KIND, EPI, RT, TT, U>),
-                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    hipLaunchKernelGGL((k_product<KIND, EPI, RT, TT, U>), grid, dim3(kThreads), (size_t)bytes, s, a);
+    a.pass_rows = (int)rows;
+    a.pass_magic = div_magic((uint32_t)rows);
+    a.dense_passes = (int)((a.num_rows + rows - 1) / rows);
+    const int64_t stride = ((int64_t)a.w.cols + F::kLine - 1) / F::kLine * F::kLine * 2 + 16;
+    // rows of several passes go to LDS together, as many as there is room for
+    int64_t x_rows = DIRECT ? kListRows : (room - sums_bytes(kWaves, kw, TT)) / (kPlanes * stride);
+    x_rows = x_rows < max_rows ? x_rows : max_rows;
+    a.x_rows = (int)(x_rows < kListRows ? x_rows : kListRows);
+    a.x_bytes = DIRECT ? 0 : (int)(a.x_rows * kPlanes * stride);
+    const int64_t lds = a.x_bytes + sums_bytes(kWaves, kw, TT);
+    if (lds > kLdsRoom) return hipErrorInvalidValue;
+    const int64_t most = kWaves == 4 ? 1 << 30 : (int64_t)num_cus();
+    const int64_t need = (tiles + kWaves / kw - 1) / (kWaves / kw);
+    const dim3 grid((unsigned)(need < most ? need : most));
+    if (lds > 32768)
+        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_product<KIND, EPI, TT, DIRECT, U, kWaves>),
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    hipLaunchKernelGGL((k_product<KIND, EPI, TT, DIRECT, U, kWaves>), grid, dim3(kWaves * kWave), (size_t)lds, s, a);
     return hipGetLastError();
 }
 
-// One kernel for the whole product.  Slots (blockIdx.y): experts that can have
-// a row, or row blocks of the dense product.
+// One kernel for the whole product.
 template <int KIND, int EPI>
 hipError_t launch_kind(const ProductArgs& a, hipStream_t s)
 {
+    using F = Format<KIND>;
     constexpr bool kPairs = EPI == kSwigluSplit || EPI == kStoreF32;
-    constexpr int U = KIND == kBf16 ? 4 : 2;
+    constexpr bool kGate = EPI == kSwigluBf16 || EPI == kSwigluSplit;
+    constexpr int kPlanes = EPI == kStoreF32 ? 2 : 1;
+    // spans of a block (2 where x or the scales take more registers)
+    constexpr int U = KIND == kInt4G32 ? 2 : 4, UD = KIND == kBf16 ? 4 : 2;
     const int64_t max_rows = kPairs || a.count ? a.P : a.num_rows;
     if (max_rows <= 0) return hipSuccess;
-    const int64_t experts = kPairs || a.count ? (max_rows < a.E ? max_rows : a.E) : 0;
-    const int64_t likely = experts ? max_rows / experts : max_rows;
-    auto slots = [&](int tt) {
-        if (experts) return (int)experts;
-        const int64_t b = (max_rows + 16 * tt - 1) / (16 * tt);
-        return (int)(b < 32768 ? b : 32768);
+    const int64_t experts = kPairs || a.count ? (max_rows < a.E ? max_rows : a.E) : 1;
+    const int64_t likely = (max_rows + experts - 1) / experts;     // rows of an expert
+    const int tt = likely > 16 ? 2 : 1;
+    // tiles of all experts' passes, if their rows are spread evenly
+    const int64_t passes = experts * ((likely + 16 * tt - 1) / (16 * tt));
+    const int64_t tiles = passes * ((a.units + (kGate ? 15 : 31)) / (kGate ? 16 : 32));
+    const int64_t stride = ((int64_t)a.w.cols + F::kLine - 1) / F::kLine * F::kLine * 2 + 16;
+    auto waves_per_tile = [&](int most, int u, int64_t want) {
+        const int64_t blocks = (a.w.row_bytes / 64 + u - 1) / u;
+        int kw = 1;
+        while (kw < most && kw * 2 <= blocks && tiles * kw < want) kw *= 2;
+        return kw;
     };
-    if (likely <= 16) return launch_shape<KIND, EPI, 2, 1, U>(a, slots(1), max_rows, s);
-    return launch_shape<KIND, EPI, 2, 4, U>(a, slots(4), max_rows, s);
+    constexpr int US = 2;
+    if (tt == 1 && tiles < 2048) {
+        const int kw = waves_per_tile(4, US, 8192);
+        const int64_t fit = (65536 - sums_bytes(4, kw, 1)) / (kPlanes * stride);
+        if (fit >= likely)
+            return launch_shape<KIND, EPI, 1, false, US, 4>(a, 65536, kw, fit < 16 ? fit : 16, max_rows, tiles, s);
+    }
+    const int kw = waves_per_tile(8, U, 8192);
+    const int64_t fit = (kLdsRoom - sums_bytes(8, kw, tt)) / (kPlanes * stride);     // rows of x in LDS
+    if (fit < (likely < 16 ? likely : 16))
+        return launch_shape<KIND, EPI, 1, true, UD, 8>(a, kLdsRoom, kw, 16, max_rows, tiles, s);
+    if (tt == 1)
+        return launch_shape<KIND, EPI, 1, false, U, 8>(a, kLdsRoom, kw, fit < 16 ? fit : 16, max_rows, tiles, s);
+    return launch_shape<KIND, EPI, 2, false, U, 8>(a, kLdsRoom, kw, fit < 32 ? fit : 32, max_rows, tiles, s);
 }
 
 template <int KIND>
