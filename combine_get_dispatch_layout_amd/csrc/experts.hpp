@@ -76,6 +76,7 @@ struct GateArgs {
     int64_t N;
     int E, K, scoring, groups, topk_groups, group_top;
     bool renorm, limit;
+    bool vec;                   // backward: rows of the gradient take vectors of four
     float scale;
     const int32_t* idx_in;      // backward
     const float* grad_w;

@@ -30,6 +30,37 @@ __device__ __forceinline__ float clean_logit(float l)
     return l == l ? fminf(l, 3.402823466e38f) : -__builtin_huge_valf();
 }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// Largest of the wave: four steps inside the rows of 16 lanes (quad_perm
+// [1,0,3,2] and [2,3,0,1], row_half_mirror, row_mirror), then the four rows.
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = fmaxf(v, dpp<0xB1>(v));
+    v = fmaxf(v, dpp<0x4E>(v));
+    v = fmaxf(v, dpp<0x141>(v));
+    v = fmaxf(v, dpp<0x140>(v));
+    return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+
 __device__ __forceinline__ double wave_sum(double v)
 {
 #pragma unroll
@@ -37,42 +68,47 @@ __device__ __forceinline__ double wave_sum(double v)
     return v;
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+// The lane whose (key, id) is the wave's highest, ties to the lower id; -1 if
+// every key is -infinity.  Rounding to fp32 keeps the order, so one fp32
+// maximum decides unless several lanes round to it; those are compared in 64
+// bits.
+__device__ __forceinline__ int wave_best(double key, int id)
 {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
-
-__device__ __forceinline__ float wave_max(float v)
-{
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
-}
-
-// Highest key of the wave, ties to the lower id; every lane gets both.
-__device__ __forceinline__ void wave_best(double& key, int& id)
-{
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        const double k = __shfl_xor(key, d);
-        const int i = __shfl_xor(id, d);
-        if (k > key || (k == key && i < id)) {
-            key = k;
-            id = i;
-        }
+    const float k = (float)key;
+    const float top = wave_max(k);
+    const bool any = key > kNone;
+    uint64_t with = __ballot(any && k == top);
+    if (with == 0) with = __ballot(any);     // all below fp32's range
+    if (with == 0) return -1;
+    int best = (int)__builtin_ctzll(with);
+    for (with &= with - 1; with != 0; with &= with - 1) {
+        const int l = (int)__builtin_ctzll(with);
+        const double kb = __shfl(key, best), kl = __shfl(key, l);
+        const int ib = __builtin_amdgcn_readlane(id, best), il = __builtin_amdgcn_readlane(id, l);
+        if (kl > kb || (kl == kb && il < ib)) best = l;
     }
+    return __builtin_amdgcn_readfirstlane(best);
+}
+
+__device__ __forceinline__ double score_of(int scoring, float l, float top, double total)
+{
+    return scoring == 0 ? exp((double)l - (double)top) / total : 1.0 / (1.0 + exp(-(double)l));
 }
 
 // One wave per token; lane l holds experts l, l + 64, ...
+// What bounds it: 64-bit arithmetic.  Every score in fp64 costs an exponential
+// and a division, so they are made only where a choice needs them (a bias,
+// groups) or the weights do (the softmax's sum); else the logits are the keys
+// and only the chosen experts' scores are computed, one a lane.
 template <int VPL>
 __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
 {
+    // groups only
     __shared__ double choice_lds[kGateWaves][VPL * kWave];
     __shared__ double key_lds[kGateWaves][VPL * kWave];
     __shared__ uint8_t out_lds[kGateWaves][VPL * kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t t = (int64_t)blockIdx.x * kGateWaves + wave;
     if (t >= a.N) return;
     int32_t* const idx = a.idx + t * a.K;
@@ -84,47 +120,49 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
         }
         return;
     }
+    constexpr float kLow = -__builtin_huge_valf();
     float l[VPL];
-    float top = -__builtin_huge_valf();
+    float top = kLow;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = lane + kWave * i;
-        l[i] = e < a.E ? clean_logit(load_logit(a.logits, a.bf16, t * a.E + e)) : -__builtin_huge_valf();
+        l[i] = e < a.E ? clean_logit(load_logit(a.logits, a.bf16, t * a.E + e)) : kLow;
         top = fmaxf(top, l[i]);
     }
-    top = wave_max(top);
-    const bool any = top > -__builtin_huge_valf();
-
-    // scores in 64 bits
-    double s[VPL], key[VPL];
-    double total = 0.0;
+    const bool groups = a.groups > 1;
+    const bool choose = a.bias != nullptr || groups;            // by scores
+    double total = 1.0;
+    if (a.scoring == 0 && (choose || !a.renorm)) {
+        top = wave_max(top);
+        total = 0.0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const bool ok = l[i] > -__builtin_huge_valf();
-        s[i] = !ok ? 0.0
-               : a.scoring == 0 ? exp((double)l[i] - (double)top) : 1.0 / (1.0 + exp(-(double)l[i]));
-        total += s[i];
-    }
-    if (a.scoring == 0 && any) {
+        for (int i = 0; i < VPL; ++i)
+            if (l[i] > kLow) total += exp((double)l[i] - (double)top);
         total = wave_sum(total);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] /= total;
     }
+
+    double key[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane + kWave * i;
-        const bool ok = l[i] > -__builtin_huge_valf();
-        double c = ok ? s[i] : kNone;
-        if (a.bias && ok) c += (double)a.bias[e];
-        if (!(c > kNone)) c = kNone;
-        key[i] = a.bias ? c : ok ? (double)l[i] : kNone;
-        if (a.groups > 1) {
-            choice_lds[wave][e] = c;
-            key_lds[wave][e] = key[i];
-            out_lds[wave][e] = 1;
+    for (int i = 0; i < VPL; ++i) key[i] = l[i] > kLow ? (double)l[i] : kNone;
+    if (choose) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = lane + kWave * i;
+            double c = kNone;
+            if (l[i] > kLow) {
+                c = score_of(a.scoring, l[i], top, total);
+                if (a.bias) c += (double)a.bias[e];
+                if (!(c > kNone)) c = kNone;
+            }
+            if (a.bias) key[i] = c;
+            if (groups) {
+                choice_lds[wave][e] = c;
+                key_lds[wave][e] = key[i];
+                out_lds[wave][e] = 1;
+            }
         }
     }
-    if (a.groups > 1) {
+    if (groups) {
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         const int per = a.E / a.groups;
@@ -138,6 +176,7 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
             for (int m = 0; m < a.group_top; ++m) {
                 double bk = kNone;
                 int bi = -1;
+#pragma unroll 4
                 for (int j = 0; j < per; ++j) {
                     const int e = lane * per + j;
                     const double k = key_lds[wave][e];
@@ -158,10 +197,9 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
         }
         uint64_t used = 0;      // the same in every lane
         for (int r = 0; r < a.topk_groups; ++r) {
-            double k = lane < a.groups && !(used >> lane & 1) ? score : kNone;
-            int id = lane;
-            wave_best(k, id);
-            if (k > kNone) used |= 1ull << id;
+            const int best = wave_best(used >> lane & 1 ? kNone : score, lane);
+            if (best < 0) break;
+            used |= 1ull << best;
         }
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -174,47 +212,44 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
         }
     }
 
-    // K times the best that is left
+    // K times the best that is left; lane k keeps the k-th
     int my_id = -1;
     float my_l = 0.f;
-    double my_s = 0.0;
-    for (int k = 0; k < a.K; ++k) {
-        double bk = kNone;
-        int bi = kMaxExperts;
-        float bl = 0.f;
-        double bs = 0.0;
+    double bk = kNone;      // this lane's best, its expert and its logit
+    int bi = kMaxExperts;
+    float bl = 0.f;
+    auto local_best = [&] {
+        bk = kNone;
+        bi = kMaxExperts;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (key[i] > bk) {
-                bk = key[i];
-                bi = lane + kWave * i;
-                bl = l[i];
-                bs = s[i];
-            }
-        double wk = bk;
-        int wi = bi;
-        wave_best(wk, wi);
-        if (!(wk > kNone)) break;
-        const int from = wi & (kWave - 1);
-        const float l_of = __shfl(bl, from);
-        const double s_of = __shfl(bs, from);
-        if (lane == k) {
-            my_id = wi;
-            my_l = l_of;
-            my_s = s_of;
+        for (int i = 0; i < VPL; ++i) {
+            const bool more = key[i] > bk;
+            bk = more ? key[i] : bk;
+            bi = more ? lane + kWave * i : bi;
+            bl = more ? l[i] : bl;
         }
+    };
+    local_best();
+    for (int k = 0; k < a.K; ++k) {
+        const int from = wave_best(bk, bi);
+        if (from < 0) break;
+        const int id = __builtin_amdgcn_readlane(bi, from);
+        const float lv = lane_value(bl, from);
+        my_id = lane == k ? id : my_id;
+        my_l = lane == k ? lv : my_l;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (lane + kWave * i == wi) key[i] = kNone;
+        for (int i = 0; i < VPL; ++i) key[i] = lane + kWave * i == id ? kNone : key[i];
+        local_best();
     }
     const bool live = my_id >= 0;
-    double v = live ? my_s : 0.0;
+    double v = 0.0;
+    if (a.scoring != 0 || !a.renorm) v = live ? score_of(a.scoring, my_l, top, total) : 0.0;
     if (a.renorm) {
-        // over the chosen alone; in the logits' differences where the scores
-        // have run out of range
-        const float lm = wave_max(live ? my_l : -__builtin_huge_valf());
-        double sum = wave_sum(v);
-        if (a.scoring == 0 || !(sum > 0.0)) {
+        // over the chosen alone; in the logits' differences for a softmax, and
+        // where sigmoids have run out of range
+        const float lm = wave_max(live ? my_l : kLow);
+        double sum = a.scoring != 0 ? wave_sum(v) : 0.0;
+        if (!(sum > 0.0)) {
             v = live ? exp((double)my_l - (double)lm) : 0.0;
             sum = wave_sum(v);
         }
@@ -232,15 +267,26 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
 //   sigmoid:              dl_e = sum over entries of g * s (1 - s)
 //   normalised sigmoid:   dl_e = sum over entries of p (1 - s) (g - sum g p)
 // HBM-bound: one pass over the logits (only the raw softmax needs them all),
-// one over the gradient.
+// one over the gradient, in vectors of four experts where rows allow it.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 template <int VPL>
 __global__ __launch_bounds__(kGateWaves* kWave) void k_gate_backward(GateArgs a)
 {
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int64_t t = (int64_t)blockIdx.x * kGateWaves + wave;
+    constexpr int V = VPL < 4 ? VPL : 4;            // neighbours in a lane
+    const int lane = threadIdx.x & (kWave - 1);
+    const int64_t t = (int64_t)blockIdx.x * kGateWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (t >= a.N) return;
     const int64_t base = t * a.E;
     const float kLow = -__builtin_huge_valf();
+    auto expert = [&](int i) { return i / V * (kWave * V) + lane * V + i % V; };
     int id = lane < a.K ? a.idx_in[t * a.K + lane] : -1;
     if ((uint32_t)id >= (uint32_t)a.E) id = -1;
     const float g = id >= 0 ? a.grad_w[t * a.K + lane] * a.scale : 0.f;
@@ -253,7 +299,7 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate_backward(GateArgs a)
         float top = kLow;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const int e = lane + kWave * i;
+            const int e = expert(i);
             p[i] = e < a.E ? clean_logit(load_logit(a.logits, a.bf16, base + e)) : kLow;
             top = fmaxf(top, p[i]);
         }
@@ -292,25 +338,40 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate_backward(GateArgs a)
         const float q = lc > 0.f ? expf(-lc) / (1.f + expf(-lc)) : 1.f / (1.f + expf(lc));
         d = pc * q * (a.renorm ? g - dot : g);
     }
+    float v[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane + kWave * i;
-        float v = 0.f;
-        for (int k = 0; k < a.K; ++k) {
-            const int ik = __builtin_amdgcn_readlane(id, k);
-            const float dk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(d), k));
-            if (ik == e) v += dk;
+    for (int i = 0; i < VPL; ++i) v[i] = 0.f;
+    for (int k = 0; k < a.K; ++k) {
+        const int ik = __builtin_amdgcn_readlane(id, k);
+        const float dk = lane_value(d, k);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] += ik == expert(i) ? dk : 0.f;
+    }
+    if (full)
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] = p[i] * (v[i] - dot);
+#pragma unroll
+    for (int i = 0; i < VPL; i += V) {
+        const int e = expert(i);
+        if (V == 4 && a.vec) {       // E % 4 == 0: whole or not at all
+            if (e >= a.E) continue;
+            if (a.bf16)
+                *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.grad_logits) + base + e) =
+                    u32x2{pack_bf16(v[i], v[i + 1 < VPL ? i + 1 : i]),
+                          pack_bf16(v[i + 2 < VPL ? i + 2 : i], v[i + 3 < VPL ? i + 3 : i])};
+            else
+                *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.grad_logits) + base + e) =
+                    f32x4{v[i], v[i + 1 < VPL ? i + 1 : i], v[i + 2 < VPL ? i + 2 : i],
+                          v[i + 3 < VPL ? i + 3 : i]};
+            continue;
         }
-        if (full) v = p[i] * (v - dot);
-        if (e < a.E) {
-            if (a.bf16) {
-                typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-                typedef float f32x2 __attribute__((ext_vector_type(2)));
-                reinterpret_cast<uint16_t*>(a.grad_logits)[base + e] = (uint16_t)__builtin_bit_cast(
-                    uint32_t, __builtin_convertvector(f32x2{v, 0.f}, bf16x2));
-            } else {
-                reinterpret_cast<float*>(a.grad_logits)[base + e] = v;
-            }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (e + j >= a.E) continue;
+            if (a.bf16)
+                reinterpret_cast<uint16_t*>(a.grad_logits)[base + e + j] = (uint16_t)pack_bf16(v[i + j], 0.f);
+            else
+                reinterpret_cast<float*>(a.grad_logits)[base + e + j] = v[i + j];
         }
     }
 }

@@ -235,6 +235,7 @@ ep_status ep_gate_backward(const ep_gate_config* cfg, const void* d_logits,
     a.idx_in = d_topk_idx;
     a.grad_w = d_grad_weights;
     a.grad_logits = d_grad_logits;
+    a.vec = a.E % 4 == 0 && aligned(d_grad_logits, a.bf16 ? 8 : 16);
     EP_HIP(epk::launch_gate_backward(a, static_cast<hipStream_t>(stream)));
     return EP_OK;
 }
