@@ -10,6 +10,23 @@ hipError_t launch_product_int4_g32(const ProductArgs& a, int epilogue, hipStream
 hipError_t launch_product_int4_g64(const ProductArgs& a, int epilogue, hipStream_t s);
 hipError_t launch_product_int4_g128(const ProductArgs& a, int epilogue, hipStream_t s);
 
+hipError_t launch_down_few_bf16(const ProductArgs& a, bool* done, hipStream_t s);
+hipError_t launch_down_few_mxfp4(const ProductArgs& a, bool* done, hipStream_t s);
+hipError_t launch_down_few_int4_g32(const ProductArgs& a, bool* done, hipStream_t s);
+hipError_t launch_down_few_int4_g64(const ProductArgs& a, bool* done, hipStream_t s);
+hipError_t launch_down_few_int4_g128(const ProductArgs& a, bool* done, hipStream_t s);
+
+hipError_t launch_down_few(const ProductArgs& a, bool* done, hipStream_t s)
+{
+    switch (a.w.kind) {
+        case kBf16: return launch_down_few_bf16(a, done, s);
+        case kMxfp4: return launch_down_few_mxfp4(a, done, s);
+        case kInt4G32: return launch_down_few_int4_g32(a, done, s);
+        case kInt4G64: return launch_down_few_int4_g64(a, done, s);
+        default: return launch_down_few_int4_g128(a, done, s);
+    }
+}
+
 hipError_t launch_product(ProductArgs a, int epilogue, hipStream_t s)
 {
     switch (a.w.kind) {

@@ -8,4 +8,9 @@ hipError_t launch_product_int4_g64(const ProductArgs& a, int epilogue, hipStream
     return prod::launch_epilogue<kInt4G64>(a, epilogue, s);
 }
 
+hipError_t launch_down_few_int4_g64(const ProductArgs& a, bool* done, hipStream_t s)
+{
+    return prod::launch_down_few<kInt4G64>(a, done, s);
+}
+
 }  // namespace epk

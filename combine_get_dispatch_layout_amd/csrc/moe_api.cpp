@@ -363,9 +363,13 @@ ep_status ep_moe_layer(const ep_handle* h, const ep_weights* w_up, const ep_weig
     down.x = reinterpret_cast<const uint16_t*>(ws + cv.act);
     down.x_lo = reinterpret_cast<const uint16_t*>(ws + cv.act_lo);
     down.ldx = w_down->cols;
-    down.y = ws + cv.y;
     down.ldy = c.hidden;
     down.flags = info.flags;
+    down.y = d_out;
+    bool done = false;
+    EP_HIP(epk::launch_down_few(down, &done, s));
+    if (done) return EP_OK;
+    down.y = ws + cv.y;
     EP_HIP(epk::launch_product(down, epk::kStoreF32, s));
 
     epk::ReduceArgs r = {};

@@ -264,6 +264,21 @@ __device__ __forceinline__ u32x4 pair_columns(u32x4 d)
                  __builtin_amdgcn_perm(d[3], d[1], 0x07060302u)};
 }
 
+__device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.f + __expf(-gate)) * up; }
+
+// y + y_lo = w * swiglu: two bf16 terms hold 16 bits of the fp32 value (an
+// infinity or NaN stays in the first), so the down projection, which takes
+// bf16 operands, loses 2^-17 of it and not 2^-9.
+__device__ __forceinline__ void store_split(const ProductArgs& a, int64_t row, int u, float gate, float up)
+{
+    const float v = swiglu(gate, up);
+    const float wv = a.weights ? a.weights[row] * v : v;
+    const uint16_t hi = to_bf16(wv);
+    const int64_t to = row * a.ldy + u;
+    reinterpret_cast<uint16_t*>(a.y)[to] = hi;
+    a.y_lo[to] = (hi & 0x7F80u) == 0x7F80u ? (uint16_t)0 : to_bf16(wv - from_bf16(hi));
+}
+
 // ---- which rows belong to which expert --------------------------------------
 //
 // Each expert's rows are taken in passes of up to pass_rows; the tiles of all
@@ -858,19 +873,10 @@ __global__ __launch_bounds__(kWaves* kWave, kWaves == 4 ? (KIND <= kMxfp4 ? 3 : 
                             const int u = unit0 + n;
                             if (u >= a.units) continue;
                             const float ga = acc[0][t][i];
-                            const float v = ga / (1.f + __expf(-ga)) * acc[1][t][i];
-                            const int64_t to = yr * a.ldy + u;
-                            if constexpr (EPI == kSwigluBf16) {
-                                reinterpret_cast<uint16_t*>(a.y)[to] = to_bf16(v);
-                            } else {
-                                // two bf16 terms hold 16 bits of the fp32 value
-                                // (an infinity or NaN stays in the first)
-                                const float wv = a.weights ? a.weights[yr] * v : v;
-                                const uint16_t hi = to_bf16(wv);
-                                reinterpret_cast<uint16_t*>(a.y)[to] = hi;
-                                a.y_lo[to] = (hi & 0x7F80u) == 0x7F80u ? (uint16_t)0
-                                                                       : to_bf16(wv - from_bf16(hi));
-                            }
+                            if constexpr (EPI == kSwigluBf16)
+                                reinterpret_cast<uint16_t*>(a.y)[yr * a.ldy + u] = to_bf16(swiglu(ga, acc[1][t][i]));
+                            else
+                                store_split(a, yr, u, ga, acc[1][t][i]);
                         } else {
 #pragma unroll
                             for (int r = 0; r < RT; ++r) {
@@ -889,6 +895,208 @@ __global__ __launch_bounds__(kWaves* kWave, kWaves == 4 ? (KIND <= kMxfp4 ? 3 : 
         at = batch_stop;
         if (at < stop) lds_barrier();      // x and the list are read; the next batch's follow
     }
+}
+
+// ---- the down projection of a handful of tokens, with the sum over their experts ---
+//
+// Up to 16 tokens and 64 pairs whose activations fit LDS.  A block owns 16
+// outputs of every token.  Row m of the A operand is token m's activation for
+// the expert whose weights are in B, so a token's experts add up in the same
+// accumulators and nothing has to be combined afterwards.  Tokens that the
+// expert is not for get any row; their sums are not kept (so that an infinity
+// or NaN in a weight stays with the tokens that chose it).  The 16 waves take
+// the (expert, block of columns) units in turn, one unit of weights ahead.
+// Latency bound: a block has few bytes (196 KB for one token, bf16, 2048 x
+// 768, top-8) and what counts is that they are asked for early.  One token
+// (GPU time of the layer): 27.7 us with the general kernel and k_layer_reduce,
+// 24.4 us with this one; MXFP4 20.6 and 16.5 us.
+constexpr int kFewWaves = 16;
+constexpr int kFewTokens = 16;
+
+// The lane's pair: its group's key, expert + kMaxExperts * (how often the
+// token listed it before), so that a group has each token once; -1: none.
+__device__ __forceinline__ int few_key(const ProductArgs& a, int e)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    const int first = lane / a.K * a.K;
+    int key = e;
+    for (int j = 1; j < a.K; ++j) {
+        const int before = __shfl_up(e, j);
+        if (e >= 0 && lane - j >= first && before == e) key += kMaxExperts;
+    }
+    return key;
+}
+
+// Token n's pair among `pairs`; -1: none.
+__device__ __forceinline__ int pair_of_token(const ProductArgs& a, uint64_t pairs, int n)
+{
+    const uint64_t of = n * a.K < kWave ? pairs >> (n * a.K) & ((1ull << a.K) - 1) : 0ull;
+    return of != 0 ? n * a.K + (int)__builtin_ctzll(of) : -1;
+}
+
+// Codes and scales of a line (both spans) of one tile's rows, past the row's
+// end zeros.  row0: the tile's first row in the stack, have: its rows.
+template <int KIND>
+struct Line {
+    u32x4 q[2];
+    SpanScale<KIND> s[2];
+};
+
+template <int KIND>
+__device__ __forceinline__ void load_line(const WeightArgs& w, int64_t row0, int have, int line, Line<KIND>& o)
+{
+    using F = Format<KIND>;
+    const int lane = threadIdx.x & (kWave - 1), n = lane & 15, c = lane >> 4;
+    const int byte = line * 128 + 16 * (lane >> 3);
+    const int row_groups = (int)w.row_groups;
+    const int64_t base = (row0 + min(n, have - 1)) * row_groups;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        o.q[v] = u32x4{0, 0, 0, 0};
+        if (byte < w.row_bytes)
+            o.q[v] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
+                w.data + (row0 + min(8 * v + (lane & 7), have - 1)) * w.row_bytes + byte));
+        if constexpr (KIND == kMxfp4) {
+            const int gi = min(line * 8 + 2 * c + v, row_groups - 1);
+            o.s[v].s[0] = __uint_as_float((uint32_t)w.scales[base + gi] << 23);
+        } else if constexpr (F::kInt4) {
+#pragma unroll
+            for (int q = 0; q < SpanScale<KIND>::kGroups; ++q) {
+                const int want = line * (256 / F::kGroup) + group_in_line<KIND>(v, q);
+                const int gi = min(want, row_groups - 1);
+                const uint32_t sc = reinterpret_cast<const uint16_t*>(w.scales)[base + gi];
+                o.s[v].s[q] = want == gi ? __uint_as_float(sc << 16) : 0.f;
+                o.s[v].off[q] = (0xC300u | (w.zeros ? w.zeros[base + gi] : 8u)) * 0x10001u;
+            }
+        }
+    }
+}
+
+template <int KIND>
+__global__ __launch_bounds__(kFewWaves* kWave, 4) void k_down_few(ProductArgs a)
+{
+    using F = Format<KIND>;
+    constexpr int kL = KIND == kBf16 ? 2 : 1;        // lines of a unit
+    extern __shared__ __align__(16) unsigned char smem[];   // the pairs' rows; later the sums
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int n = lane & 15, c = lane >> 4;
+    const int row_bytes = (int)a.w.row_bytes;
+    const int cols_up = (a.w.cols + F::kLine - 1) / F::kLine * F::kLine;
+    const int stride = cols_up * 2 + 16;
+    const int lo_bytes = a.P * stride;
+
+    int e = lane < a.P ? a.topk[lane] : -1;
+    if ((uint32_t)e >= (uint32_t)a.E) e = -1;        // flagged by the up projection
+    const int key = few_key(a, e);
+    const uint64_t firsts = first_pairs(key, a.P);
+    const int per = (row_bytes + 128 * kL - 1) / (128 * kL);     // units of an expert
+    const int units = __popcll(firsts) * per;
+    const int tile0 = blockIdx.x * 16;
+
+    struct Unit {
+        Line<KIND> w[kL];
+        int line;
+        uint64_t pairs;
+    };
+    const int have = min(16, a.units - tile0);
+    auto load = [&](int u, Unit& o) {
+        const int group = u / per;
+        int k;
+        find_few(key, firsts, group, &k, &o.pairs);
+        o.line = (u - group * per) * kL;
+#pragma unroll
+        for (int l = 0; l < kL; ++l)
+            load_line<KIND>(a.w, (int64_t)(k % kMaxExperts) * a.w.rows + tile0, have, o.line + l, o.w[l]);
+    };
+    Unit cur, next;
+    if (wave < units) load(wave, cur);
+
+    // ---- activations to LDS
+    const int vecs = cols_up / 8;
+    for (int m = wave; m < a.P; m += kFewWaves) {
+        if (__builtin_amdgcn_readlane(e, m) < 0) continue;      // never read
+        for (int v = lane; v < vecs; v += kWave)
+#pragma unroll
+            for (int pl = 0; pl < 2; ++pl) {
+                u32x4 d = {0, 0, 0, 0};
+                if (v * 8 < a.w.cols)
+                    d = *reinterpret_cast<const u32x4*>((pl ? a.x_lo : a.x) + (int64_t)m * a.ldx + v * 8);
+                if constexpr (F::kInt4) d = pair_columns(d);
+                *reinterpret_cast<u32x4*>(smem + pl * lo_bytes + m * stride + 16 * v) = d;
+            }
+    }
+    lds_barrier();
+
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int u = wave; u < units; u += kFewWaves) {
+        if (u + kFewWaves < units) load(u + kFewWaves, next);
+        // token n's pair of this group; none: any
+        const int mine = pair_of_token(a, cur.pairs, n);
+        const int m = mine >= 0 ? mine : (int)__builtin_ctzll(cur.pairs);
+        f32x4 part = {0.f, 0.f, 0.f, 0.f};
+        const unsigned char* xa = smem + m * stride + c * F::kLaneBytes;
+#pragma unroll
+        for (int ln = 0; ln < kL; ++ln) {
+            if (ln > 0 && (cur.line + ln) * 128 >= row_bytes) break;
+            u32x4 q[2];
+            trade_halves(cur.w[ln].q[0], cur.w[ln].q[1], q[0], q[1]);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                u32x4 b[F::kParts], x[2 * F::kParts];
+                const unsigned char* p = xa + (cur.line + ln) * F::kLineBytes + v * F::kSpanBytes;
+#pragma unroll
+                for (int j = 0; j < F::kParts; ++j) {
+                    x[j] = *reinterpret_cast<const u32x4*>(p + j * F::kPartBytes);
+                    x[F::kParts + j] = *reinterpret_cast<const u32x4*>(p + lo_bytes + j * F::kPartBytes);
+                }
+                expand<KIND>(q[v], cur.w[ln].s[v], b);
+                multiply<KIND, true>(b, cur.w[ln].s[v], x, part);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = pair_of_token(a, cur.pairs, 4 * c + i) >= 0 ? acc[i] + part[i] : acc[i];
+        cur = next;
+    }
+
+    // ---- the waves' shares, added in wave order
+    lds_barrier();
+    f32x4* const red = reinterpret_cast<f32x4*>(smem);
+    red[wave * kWave + lane] = acc;
+    lds_barrier();
+    if (wave != 0) return;
+    f32x4 sum = red[lane];
+    for (int w = 1; w < kFewWaves; ++w) sum += red[w * kWave + lane];
+    const int tokens = a.P / a.K;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (4 * c + i < tokens && tile0 + n < a.units)
+            reinterpret_cast<uint16_t*>(a.y)[(int64_t)(4 * c + i) * a.ldy + tile0 + n] = to_bf16(sum[i]);
+}
+
+// LDS of k_down_few.
+template <int KIND>
+int64_t few_bytes(const ProductArgs& a)
+{
+    using F = Format<KIND>;
+    const int64_t stride = ((int64_t)a.w.cols + F::kLine - 1) / F::kLine * F::kLine * 2 + 16;
+    const int64_t x = 2 * (int64_t)a.P * stride, red = (int64_t)kFewWaves * kWave * 16;
+    return x > red ? x : red;
+}
+
+// The down projection and the sum over experts in one kernel, if the batch is
+// a handful (*done); the caller takes the general path otherwise.
+template <int KIND>
+hipError_t launch_down_few(const ProductArgs& a, bool* done, hipStream_t s)
+{
+    const int64_t lds = few_bytes<KIND>(a);
+    *done = a.P <= kWave && a.P / a.K <= kFewTokens && lds <= 65536;
+    if (!*done) return hipSuccess;
+    if (lds > 32768)
+        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_down_few<KIND>),
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    hipLaunchKernelGGL(k_down_few<KIND>, dim3((a.units + 15) / 16), dim3(kFewWaves * kWave), (size_t)lds, s, a);
+    return hipGetLastError();
 }
 
 // ---- launch -------------------------------------------------------------
@@ -943,6 +1151,9 @@ hipError_t launch_shape(ProductArgs a, int64_t room, int kw, int64_t rows, int64
     return hipGetLastError();
 }
 
+// Waves of the big blocks (one of eight waves a CU) that run at a time.
+constexpr int64_t kAtOnce = 2048;
+
 // One kernel for the whole product.
 template <int KIND, int EPI>
 hipError_t launch_kind(const ProductArgs& a, hipStream_t s)
@@ -962,20 +1173,25 @@ hipError_t launch_kind(const ProductArgs& a, hipStream_t s)
     const int64_t passes = experts * ((likely + 16 * tt - 1) / (16 * tt));
     const int64_t tiles = passes * ((a.units + (kGate ? 15 : 31)) / (kGate ? 16 : 32));
     const int64_t stride = ((int64_t)a.w.cols + F::kLine - 1) / F::kLine * F::kLine * 2 + 16;
-    auto waves_per_tile = [&](int most, int u, int64_t want) {
+    // waves of a team: as long as all waves' work fits the GPU at once
+    auto waves_per_tile = [&](int most, int u, int64_t at_once) {
         const int64_t blocks = (a.w.row_bytes / 64 + u - 1) / u;
         int kw = 1;
-        while (kw < most && kw * 2 <= blocks && tiles * kw < want) kw *= 2;
+        while (kw < most && kw * 2 <= blocks && tiles * kw * 2 <= at_once) kw *= 2;
         return kw;
     };
+    // Few tiles (less than one a wave of the big blocks): blocks of four waves
+    // and short rings, three to a CU.  One token through the bf16 layer's up
+    // projection takes 14.6 us so and 17.8 us with the big blocks; a decode
+    // batch's (32768 tiles) 1374 and 667 us.
     constexpr int US = 2;
-    if (tt == 1 && tiles < 2048) {
-        const int kw = waves_per_tile(4, US, 8192);
+    if (tt == 1 && tiles < kAtOnce) {
+        const int kw = waves_per_tile(4, US, 4 * kAtOnce);
         const int64_t fit = (65536 - sums_bytes(4, kw, 1)) / (kPlanes * stride);
         if (fit >= likely)
             return launch_shape<KIND, EPI, 1, false, US, 4>(a, 65536, kw, fit < 16 ? fit : 16, max_rows, tiles, s);
     }
-    const int kw = waves_per_tile(8, U, 8192);
+    const int kw = waves_per_tile(8, U, kAtOnce);
     const int64_t fit = (kLdsRoom - sums_bytes(8, kw, tt)) / (kPlanes * stride);     // rows of x in LDS
     if (fit < (likely < 16 ? likely : 16))
         return launch_shape<KIND, EPI, 1, true, UD, 8>(a, kLdsRoom, kw, 16, max_rows, tiles, s);

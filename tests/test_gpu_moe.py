@@ -380,6 +380,49 @@ def test_layer(N, E, K, H, I, mask, dup, skew, fmt, group, zeros):
     assert (out[N:] == 77).all()
 
 
+@pytest.mark.parametrize("N,E,K,H,I,mask", [
+    (4, 3, 4, 128, 128, 0.2),        # one expert several times in a row
+    (3, 2, 16, 128, 128, 0.0),
+    (16, 5, 4, 384, 128, 0.1),       # 16 tokens, 64 pairs: the most of a handful
+    (13, 5, 5, 256, 128, 0.1),       # 65 pairs: one more
+    (17, 5, 2, 256, 128, 0.0),       # 17 tokens
+    (8, 4, 8, 128, 512, 0.0),        # activations past 64 KB
+])
+@pytest.mark.parametrize("fmt,group", [("bf16", 0), ("mxfp4", 32), ("int4", 128)])
+def test_layer_handful(N, E, K, H, I, mask, fmt, group):
+    """Around the limits of the batches that are summed inside the down
+    projection, with ids listed more than once."""
+    say(f"[layer handful] {N} {E} {K} {H} {I} {fmt}")
+    c = layer_case(N, E, K, H, I, fmt, group, seed=N + K, mask=mask, dup=True)
+    R.assert_close(run_layer(c), c["want"], c["err"])
+
+
+@pytest.mark.parametrize("N", [5, 24])
+def test_layer_keeps_nan_with_the_tokens_that_chose_it(N):
+    """An expert of NaN weights (and a NaN row of x): the other tokens do not
+    see them."""
+    for fmt, group in (("bf16", 0), ("mxfp4", 32), ("int4", 64)):
+        c = layer_case(N, 6, 2, 128, 64, fmt, group, seed=3)
+        idx = c["idx"].cpu().numpy()
+        idx[idx == 5] = 4
+        idx[2] = [5, 1]
+        c["idx"].copy_(torch.from_numpy(idx))
+        want = run_layer(c).clone()
+        assert torch.isfinite(want).all()
+        for w in (c["up"], c["down"]):
+            if fmt == "bf16":
+                w.data[5] = float("nan")
+            elif fmt == "mxfp4":
+                w.scales[5] = 255
+            else:
+                w.scales[5] = float("inf")
+        c["x"][N - 1] = float("nan")
+        got = run_layer(c)
+        keep = [t for t in range(N) if t not in (2, N - 1)]
+        assert torch.equal(got[keep], want[keep]), fmt
+        assert not torch.isfinite(got[2]).any() and torch.isnan(got[N - 1]).all()
+
+
 @pytest.mark.parametrize("fmt,H,I", [("bf16", 72, 40), ("bf16", 8, 8), ("mxfp4", 96, 32), ("mxfp4", 32, 160)])
 @pytest.mark.parametrize("N", [1, 5, 20])
 def test_layer_odd_sizes(N, fmt, H, I):
