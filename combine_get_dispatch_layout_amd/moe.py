@@ -11,7 +11,8 @@ from typing import Optional
 
 import torch
 
-from .ep import Handle, _check, _check_tensor, _ptr, _stream, lib
+from . import ep
+from .ep import EP_OK, Handle, _check, lib
 
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 EP_LOGITS_FP32, EP_LOGITS_BF16 = 0, 1
@@ -42,8 +43,9 @@ _bound = None
 def _lib():
     """ep.py's library with this header's signatures set."""
     global _bound
-    L = lib()
-    if _bound is not L:
+    L = ep._lib
+    if L is None or _bound is not L:
+        L = lib()
         P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
         L.ep_gate.argtypes = [P, P, P, P, I64, P, P, P]
         L.ep_gate_backward.argtypes = [P, P, P, P, I64, P, P]
@@ -57,13 +59,33 @@ def _lib():
     return L
 
 
+def _check_tensor(name, t, dtypes, shape, device):
+    """ep._check_tensor, with its tests in an order that costs a good call
+    little: these calls take as long on the host as on the GPU."""
+    if t is not None and not (t.dtype in dtypes and t.shape == shape and t.device == device):
+        ep._check_tensor(name, t, dtypes, shape, device)
+
+
+def _ptr(t):
+    """The address of a contiguous GPU tensor as an int (None for None)."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        ep._ptr(t)                  # raises
+    return t.data_ptr()
+
+
 def _call(device, fn, *args):
-    """fn(*args, stream) with the tensors' device current."""
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, _stream(device)))
+    """fn(*args, stream) on the device's current stream, with the device
+    current."""
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(device)))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != EP_OK:
+        _check(st)
 
 
 # ---- router ----------------------------------------------------------------
@@ -132,7 +154,7 @@ def ep_gate_backward(cfg: GateConfig, logits: torch.Tensor, topk_idx: torch.Tens
     _check_tensor("topk_idx", topk_idx, (torch.int32,), (N, cfg.num_topk), dev)
     _check_tensor("grad_weights", grad_weights, (torch.float32,), (N, cfg.num_topk), dev)
     if grad_logits is None:
-        grad_logits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+        grad_logits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
     else:
         _check_tensor("grad_logits", grad_logits, (logits.dtype,), logits.shape, dev)
     _call(dev, _lib().ep_gate_backward, cfg.c(logits.dtype), _ptr(logits), _ptr(topk_idx),
@@ -240,7 +262,7 @@ def ep_moe_layer(h: Handle, w_up: Weights, w_down: Weights, x: torch.Tensor,
     _check_tensor("topk_idx", topk_idx, (torch.int32,), (N, cfg.num_topk), dev)
     _check_tensor("topk_weights", topk_weights, (torch.float32,), (N, cfg.num_topk), dev)
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
         _check_tensor("out", out, (torch.bfloat16,), x.shape, dev)
     if workspace is None:
