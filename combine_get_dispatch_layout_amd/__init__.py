@@ -2,8 +2,9 @@
 assignment, dispatch (optionally FP8 E4M3FN / int8 quantised) and weighted
 combine, with the router, products with (4-bit) expert weights and the whole
 expert layer for a few tokens beside them, as hand-written HIP kernels for
-gfx950 behind a C ABI (include/ep.h, include/ep_moe.h).  This package holds the kernels (csrc/), their build script
-and the thin Python binding (ep.py, moe.py)."""
+gfx950 behind a C ABI (include/ep.h, include/ep_moe.h).  This package holds the
+kernels (csrc/), their build script and the thin Python binding (ep.py,
+moe.py)."""
 from .ep import (Config, EpError, Handle, ep_check_error, ep_combine, ep_dispatch,  # noqa: F401
                  ep_get_layout, ep_handle_free, ep_handle_get_view, ep_handle_init,
                  ep_layout_dispatch, ep_quantize_rows, ep_dispatch_topk, ep_dispatch_overlap,

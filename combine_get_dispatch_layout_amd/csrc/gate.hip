@@ -99,7 +99,9 @@ __device__ __forceinline__ double score_of(int scoring, float l, float top, doub
 // What bounds it: 64-bit arithmetic.  Every score in fp64 costs an exponential
 // and a division, so they are made only where a choice needs them (a bias,
 // groups) or the weights do (the softmax's sum); else the logits are the keys
-// and only the chosen experts' scores are computed, one a lane.
+// and only the chosen experts' scores are computed, one a lane.  8192 tokens,
+// 256 experts in 32 groups, sigmoid and bias: 23.3 us (33.7 with 64-bit
+// exchanges in every reduction); one token without groups 4.9 us (9.9).
 template <int VPL>
 __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
 {
@@ -267,7 +269,8 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
 //   sigmoid:              dl_e = sum over entries of g * s (1 - s)
 //   normalised sigmoid:   dl_e = sum over entries of p (1 - s) (g - sum g p)
 // HBM-bound: one pass over the logits (only the raw softmax needs them all),
-// one over the gradient, in vectors of four experts where rows allow it.
+// one over the gradient, in vectors of four experts where rows allow it.  8191
+// tokens, 256 experts, fp32: 7.7 us (9.9 with single stores), 2.2 TB/s.
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));

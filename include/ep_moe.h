@@ -126,7 +126,8 @@ typedef struct ep_weights {
 /* y = act(x W^T) for num_rows rows and one matrix (num_experts == 1):
  *   d_x bf16 [num_rows, cols], 16-byte aligned; d_y bf16 [num_rows, M] (or
  *   [num_rows, M/2] with EP_ACT_SWIGLU), not overlapping x.  Sums in fp32, one
- *   rounding to bf16.  For few rows: the weights are read once per 64 rows. */
+ *   rounding to bf16.  Made for few rows: the weights are read once per pass of
+ *   up to 16 rows (32 where there are more); num_rows * M below 2^35. */
 ep_status ep_matvec(const ep_weights* w, const void* d_x, int64_t num_rows, int32_t activation,
                     void* d_y, void* stream);
 
@@ -136,7 +137,8 @@ ep_status ep_matvec(const ep_weights* w, const void* d_x, int64_t num_rows, int3
  *   earlier product's y), d_y bf16 [x_rows, M or M/2].  Rows that hold no token
  *   (alignment padding, unfilled capacity, rows behind the last segment) are
  *   neither read nor written.  Rows at or beyond x_rows are skipped and flagged
- *   EP_FLAG_RECV_CAPACITY (ep_check_error).  w->num_experts is the handle's;
+ *   EP_FLAG_RECV_CAPACITY (ep_check_error); x_rows * M below 2^35.  Per expert
+ *   passes of rows as in ep_matvec.  w->num_experts is the handle's;
  *   the handle has a finished layout (EP_ERR_STATE) in the expand form
  *   (EP_ERR_INVALID_ARG for non_expand, whose rows belong to ranks). */
 ep_status ep_expert_matvec(const ep_handle* h, const ep_weights* w, const void* d_x,
@@ -165,7 +167,9 @@ ep_status ep_moe_workspace_size(const ep_handle* h, const ep_weights* w_up,
  *   expert gets +0.  d_out may be d_x.
  *   d_workspace: 256-byte aligned, at least ep_moe_workspace_size bytes, needs
  *   no clearing; in use by one stream (or graph in flight) at a time.
- *   The result does not depend on the order in which blocks run. */
+ *   Two kernels for up to 16 tokens and 64 entries of topk_idx whose activations
+ *   fit LDS (64 KB: 4 bytes * entries * I), else three.  The result does not
+ *   depend on the order in which blocks run. */
 ep_status ep_moe_layer(const ep_handle* h, const ep_weights* w_up, const ep_weights* w_down,
                        const void* d_x, const int32_t* d_topk_idx, const float* d_topk_weights,
                        int64_t num_tokens, void* d_out, void* d_workspace, int64_t workspace_bytes,
