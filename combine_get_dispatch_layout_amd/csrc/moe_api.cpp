@@ -111,6 +111,8 @@ ep_status check_weights(const ep_weights* w, const char* name, bool pointers)
                                                    : "16-byte aligned and not NULL");
     if (w->d_zeros && w->format != EP_WEIGHT_INT4)
         return EP_FAIL(EP_ERR_INVALID_ARG, "%s: only INT4 weights have zeros", name);
+    if (!aligned(w->d_zeros, 16))
+        return EP_FAIL(EP_ERR_INVALID_ARG, "%s: zeros must be 16-byte aligned", name);
     return EP_OK;
 }
 
@@ -175,6 +177,11 @@ ep_status check_layer(const ep_handle* h, const ep_weights* up, const ep_weights
     if (num_tokens < 0 || num_tokens > EP_MOE_MAX_TOKENS)
         return EP_FAIL(EP_ERR_INVALID_ARG, "num_tokens=%lld outside [0,%d]", (long long)num_tokens,
                        EP_MOE_MAX_TOKENS);
+    // the kernels number (row, 16 outputs) tiles in 32 bits
+    const int64_t outputs = up->rows > down->rows ? up->rows : down->rows;
+    if (num_tokens * c.num_topk * ((outputs + 15) / 16) >= (int64_t)1 << 31)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "%lld pairs times %lld outputs above 2^35",
+                       (long long)(num_tokens * c.num_topk), (long long)outputs);
     return EP_OK;
 }
 

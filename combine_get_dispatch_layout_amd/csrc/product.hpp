@@ -435,7 +435,7 @@ constexpr int kListRows = 128;      // ... and their rows, at most
 // tile and its up tile); TT: 16-row tiles of x.
 // DIRECT: x is read from memory, a block ahead, not through LDS.
 template <int KIND, int EPI, int TT, bool DIRECT, int kU, int kWaves>
-__global__ __launch_bounds__(kWaves* kWave, kWaves == 4 ? (KIND <= kMxfp4 ? 3 : 2) : kWaves / 4) void k_product(ProductArgs a)
+__global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kWaves == 4 ? (KIND <= kMxfp4 ? 3 : 2) : kWaves / 4) void k_product(ProductArgs a)
 {
     constexpr int kThreads = kWaves * kWave;
     using F = Format<KIND>;
@@ -611,7 +611,7 @@ __global__ __launch_bounds__(kWaves* kWave, kWaves == 4 ? (KIND <= kMxfp4 ? 3 : 
             if constexpr (kPairs) return a.x_per_pair ? row : row / a.K;
             else return row;
         };
-        const int lo_bytes = a.x_rows * stride;
+        const int lo_bytes = DIRECT ? 0 : a.x_rows * stride;
         if constexpr (!DIRECT) {
             const int vecs = cols_up / 8;
             for (int m = wave; m < lds_rows; m += kWaves) {
@@ -1153,7 +1153,7 @@ hipError_t launch_shape(ProductArgs a, int64_t room, int kw, int64_t rows, int64
     a.x_bytes = DIRECT ? 0 : (int)(a.x_rows * kPlanes * stride);
     const int64_t lds = a.x_bytes + sums_bytes(kWaves, kw, TT);
     if (lds > kLdsRoom) return hipErrorInvalidValue;
-    const int64_t most = kWaves == 4 ? 1 << 30 : (int64_t)num_cus();
+    const int64_t most = kWaves == 4 && TT == 1 ? 1 << 30 : (int64_t)num_cus();
     const int64_t need = (tiles + kWaves / kw - 1) / (kWaves / kw);
     const dim3 grid((unsigned)(need < most ? need : most));
     if (lds > 32768)
@@ -1209,7 +1209,10 @@ hipError_t launch_kind(const ProductArgs& a, hipStream_t s)
         return launch_shape<KIND, EPI, 1, true, UD, 8>(a, kLdsRoom, kw, 16, max_rows, tiles, s);
     if (tt == 1)
         return launch_shape<KIND, EPI, 1, false, U, 8>(a, kLdsRoom, kw, fit < 16 ? fit : 16, max_rows, tiles, s);
-    return launch_shape<KIND, EPI, 2, false, U, 8>(a, kLdsRoom, kw, fit < 32 ? fit : 32, max_rows, tiles, s);
+    // INT4 with two row tiles needs more than the 256 registers of eight waves
+    constexpr int W2 = F::kInt4 ? 4 : 8;
+    return launch_shape<KIND, EPI, 2, false, U, W2>(a, kLdsRoom, kw < W2 ? kw : W2, fit < 32 ? fit : 32, max_rows,
+                                                    tiles, s);
 }
 
 template <int KIND>

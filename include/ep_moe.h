@@ -109,7 +109,7 @@ enum {
 #define EP_MOE_MAX_TOKENS 256
 
 /* A stack of weight matrices, row-major, contiguous, in caller-owned device
- * memory: d_data and (MXFP4, INT4) d_scales 16-byte aligned. */
+ * memory, each 16-byte aligned. */
 typedef struct ep_weights {
     int32_t format;        /* EP_WEIGHT_*                                      */
     int32_t group;         /* columns per scale: 0 (BF16), 32 (MXFP4), 32, 64 or

@@ -1,5 +1,7 @@
 """GPU tests of the router, the products with expert weights and the whole
 expert layer against their plain 64-bit definitions (moe_reference)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -573,6 +575,61 @@ def test_large_offsets():
         y = moe.ep_expert_matvec(h, moe.Weights(FMT[fmt], d, s), x)
         want, err = R.product(x.double().cpu().numpy(), w64[0], mag[0], R.terms(C, 0), 0)
         R.assert_close(y, want, err, fmt)
+
+
+# ---- refusals that need a handle (the pointers are never used) -------------------
+
+PTR = 0x10000
+
+
+def _w(**kw):
+    return moe.ep_weights(*{**dict(format=moe.EP_WEIGHT_INT4, group=32, num_experts=1, rows=64, cols=128,
+                                   reserved=0, d_data=PTR, d_scales=PTR, d_zeros=None), **kw}.values())
+
+
+@pytest.mark.parametrize("up,down,n,ok", [
+    ({}, {}, 256, True), ({}, {}, 257, False), ({}, {}, -1, False),
+    (dict(rows=96), {}, 4, False), (dict(cols=256), {}, 4, False), ({}, dict(rows=256), 4, False),
+    (dict(num_experts=3), {}, 4, False), ({}, dict(num_experts=5), 4, False), (dict(rows=63), {}, 4, False),
+])
+def test_layer_sizes(up, down, n, ok):
+    """The layer's stacks against the handle: refused before anything runs."""
+    h = ep.ep_handle_init(ep.Config(hidden=128, num_topk=2, num_experts=4, num_ranks=1), 1)
+    raw = h.ptr
+    wu = _w(**{**dict(num_experts=4, rows=64, cols=128), **up})
+    wd = _w(**{**dict(num_experts=4, rows=128, cols=32), **down})
+    out = ctypes.c_int64(-1)
+    st = moe._lib().ep_moe_workspace_size(raw, ctypes.byref(wu), ctypes.byref(wd), n, ctypes.byref(out))
+    assert st == (ep.EP_OK if ok else ep.EP_ERR_INVALID_ARG)
+    if ok:      # two terms of the activations and each pair's output
+        assert out.value >= n * 2 * (4 * 32 + 4 * 128) and out.value % 256 == 0
+    else:
+        assert moe._lib().ep_moe_layer(raw, ctypes.byref(wu), ctypes.byref(wd), PTR, PTR, PTR, n, PTR, PTR,
+                                       1 << 30, None) == ep.EP_ERR_INVALID_ARG
+
+
+def test_layer_refuses_sizes_past_32_bits_and_bad_pointers():
+    held = ep.ep_handle_init(ep.Config(hidden=1 << 24, num_topk=16, num_experts=4, num_ranks=1), 1)
+    big = held.ptr
+    wu = _w(num_experts=4, rows=64, cols=1 << 24)
+    wd = _w(num_experts=4, rows=1 << 24, cols=32)
+    L, out = moe._lib(), ctypes.c_int64()
+    assert L.ep_moe_workspace_size(big, ctypes.byref(wu), ctypes.byref(wd), 256, ctypes.byref(out)) == \
+        ep.EP_ERR_INVALID_ARG
+    assert L.ep_moe_workspace_size(big, ctypes.byref(wu), ctypes.byref(wd), 64, ctypes.byref(out)) == ep.EP_OK
+    small = ep.ep_handle_init(ep.Config(hidden=128, num_topk=2, num_experts=4, num_ranks=1), 1)
+    h = small.ptr
+    wu, wd = _w(num_experts=4, rows=64, cols=128), _w(num_experts=4, rows=128, cols=32)
+    good = [PTR, PTR, PTR, 4, PTR, PTR, 1 << 30]
+    for i, v in ((0, None), (0, PTR + 8), (1, None), (1, PTR + 2), (2, PTR + 2), (4, None), (4, PTR + 8)):
+        a = list(good)
+        a[i] = v
+        assert L.ep_moe_layer(h, ctypes.byref(wu), ctypes.byref(wd), *a, None) == ep.EP_ERR_INVALID_ARG
+    for i, v in ((5, None), (5, PTR + 128), (6, 1000)):
+        a = list(good)
+        a[i] = v
+        assert L.ep_moe_layer(h, ctypes.byref(wu), ctypes.byref(wd), *a, None) == ep.EP_ERR_WORKSPACE
+    assert L.ep_moe_layer(h, ctypes.byref(wu), ctypes.byref(wd), None, None, None, 0, None, None, 0, None) == ep.EP_OK
 
 
 # ---- together -------------------------------------------------------------------

@@ -79,7 +79,7 @@ BAD_WEIGHTS = [
     dict(format=3), dict(format=-1), dict(num_experts=0), dict(num_experts=1025), dict(rows=0),
     dict(rows=(1 << 24) + 1), dict(cols=0), dict(cols=(1 << 24) + 32), dict(reserved=1), dict(group=16),
     dict(group=256), dict(group=0), dict(cols=144), dict(group=128, cols=192), dict(d_data=None),
-    dict(d_data=PTR + 8), dict(d_scales=None), dict(d_scales=PTR + 8),
+    dict(d_data=PTR + 8), dict(d_scales=None), dict(d_scales=PTR + 8), dict(d_zeros=PTR + 4),
     dict(format=moe.EP_WEIGHT_MXFP4, group=64), dict(format=moe.EP_WEIGHT_MXFP4, d_zeros=PTR),
     dict(format=moe.EP_WEIGHT_BF16), dict(format=moe.EP_WEIGHT_BF16, group=0),          # scales
     dict(format=moe.EP_WEIGHT_BF16, group=0, d_scales=None, cols=100),
