@@ -75,6 +75,8 @@ struct GateArgs {
     const uint8_t* mask;
     int64_t N;
     int E, K, scoring, groups, topk_groups, group_top;
+    int per;                    // experts of a group
+    uint32_t per_magic;         // div_magic(per)
     bool renorm, limit;
     bool vec;                   // backward: rows of the gradient take vectors of four
     float scale;

@@ -16,6 +16,7 @@ namespace epk {
 namespace {
 
 constexpr int kGateWaves = 4;
+constexpr int kMaxGroups = 64;
 constexpr double kNone = -__builtin_huge_val();
 
 __device__ __forceinline__ float load_logit(const void* p, bool bf16, int64_t i)
@@ -100,15 +101,17 @@ __device__ __forceinline__ double score_of(int scoring, float l, float top, doub
 // and a division, so they are made only where a choice needs them (a bias,
 // groups) or the weights do (the softmax's sum); else the logits are the keys
 // and only the chosen experts' scores are computed, one a lane.  8192 tokens,
-// 256 experts in 32 groups, sigmoid and bias: 23.3 us (33.7 with 64-bit
+// 256 experts in 32 groups, sigmoid and bias: 22.4 us (33.7 with 64-bit
 // exchanges in every reduction); one token without groups 4.9 us (9.9).
 template <int VPL>
 __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
 {
-    // groups only
-    __shared__ double choice_lds[kGateWaves][VPL * kWave];
-    __shared__ double key_lds[kGateWaves][VPL * kWave];
-    __shared__ uint8_t out_lds[kGateWaves][VPL * kWave];
+    // groups only; expert e at e + its group, so that the lanes of the search,
+    // one a group, start in different banks
+    constexpr int kSlots = VPL * kWave + kMaxGroups;
+    __shared__ double choice_lds[kGateWaves][kSlots];
+    __shared__ double key_lds[kGateWaves][kSlots];
+    __shared__ uint8_t out_lds[kGateWaves][kSlots];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t t = (int64_t)blockIdx.x * kGateWaves + wave;
@@ -143,6 +146,7 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
         total = wave_sum(total);
     }
 
+    auto group_of = [&](int e) { return a.per_magic ? (int)__umulhi((uint32_t)e, a.per_magic) : e; };
     double key[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] = l[i] > kLow ? (double)l[i] : kNone;
@@ -157,45 +161,51 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
                 if (!(c > kNone)) c = kNone;
             }
             if (a.bias) key[i] = c;
-            if (groups) {
-                choice_lds[wave][e] = c;
-                key_lds[wave][e] = key[i];
-                out_lds[wave][e] = 1;
+            if (groups && e < a.E) {
+                const int to = e + group_of(e);
+                choice_lds[wave][to] = c;
+                key_lds[wave][to] = key[i];
+                out_lds[wave][to] = 1;
             }
         }
     }
     if (groups) {
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const int per = a.E / a.groups;
+        const int per = a.per;
         double score = kNone;
         if (lane < a.groups) {
-            // the best group_top members in order: each the first after the last
+            // the best group_top members in order, two a pass: those after the
+            // last pair.  Going up in e, a later equal key never comes first.
             double lk = __builtin_huge_val();
             int li = -1;
-            bool got = false;
             double sum = 0.0;
-            for (int m = 0; m < a.group_top; ++m) {
-                double bk = kNone;
-                int bi = -1;
+            const int base = lane * (per + 1);
+            for (int m = 0; m < a.group_top; m += 2) {
+                double k1 = kNone, k2 = kNone;
+                int i1 = -1, i2 = -1;
 #pragma unroll 4
                 for (int j = 0; j < per; ++j) {
-                    const int e = lane * per + j;
-                    const double k = key_lds[wave][e];
-                    const bool after = li < 0 || k < lk || (k == lk && e > li);
-                    if (after && k > bk) {
-                        bk = k;
-                        bi = e;
-                    }
+                    const double kj = key_lds[wave][base + j];
+                    const bool after = li < 0 || kj < lk || (kj == lk && j > li);
+                    const double k = after ? kj : kNone;
+                    const bool best = k > k1, second = k > k2;
+                    k2 = best ? k1 : second ? k : k2;
+                    i2 = best ? i1 : second ? j : i2;
+                    k1 = best ? k : k1;
+                    i1 = best ? j : i1;
                 }
-                if (bi < 0) break;
-                sum += choice_lds[wave][bi];
-                if (a.limit) out_lds[wave][bi] = 2;
-                got = true;
-                lk = bk;
-                li = bi;
+                if (i1 < 0) break;
+                sum += choice_lds[wave][base + i1];
+                if (a.limit) out_lds[wave][base + i1] = 2;
+                score = sum;
+                if (i2 < 0 || m + 1 == a.group_top) break;
+                sum += choice_lds[wave][base + i2];
+                if (a.limit) out_lds[wave][base + i2] = 2;
+                score = sum;
+                lk = k2;
+                li = i2;
             }
-            if (got) score = sum;
         }
         uint64_t used = 0;      // the same in every lane
         for (int r = 0; r < a.topk_groups; ++r) {
@@ -208,8 +218,8 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             const int e = lane + kWave * i;
-            const int group = e < a.E ? e / per : 0;
-            const uint32_t keeps = (uint32_t)(used >> group) & (a.limit ? out_lds[wave][e] >> 1 : 1u);
+            const int at = e < a.E ? e : 0, group = group_of(at);
+            const uint32_t keeps = (uint32_t)(used >> group) & (a.limit ? out_lds[wave][at + group] >> 1 : 1u);
             key[i] = (keeps & 1u) != 0u ? key[i] : kNone;
         }
     }

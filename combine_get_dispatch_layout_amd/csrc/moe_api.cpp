@@ -70,6 +70,8 @@ ep_status check_gate(const ep_gate_config* c, int64_t num_tokens, epk::GateArgs*
     a.groups = c->num_groups;
     a.topk_groups = c->topk_groups;
     a.group_top = c->group_top;
+    a.per = c->num_groups > 1 ? c->num_experts / c->num_groups : 1;
+    a.per_magic = epk::div_magic((uint32_t)a.per);
     a.limit = c->group_limit == 1;
     a.scale = c->scale;
     return EP_OK;
