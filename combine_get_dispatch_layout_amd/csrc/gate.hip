@@ -101,8 +101,9 @@ __device__ __forceinline__ double score_of(int scoring, float l, float top, doub
 // and a division, so they are made only where a choice needs them (a bias,
 // groups) or the weights do (the softmax's sum); else the logits are the keys
 // and only the chosen experts' scores are computed, one a lane.  8192 tokens,
-// 256 experts in 32 groups, sigmoid and bias: 22.4 us (33.7 with 64-bit
-// exchanges in every reduction); one token without groups 4.9 us (9.9).
+// 256 experts in 32 groups, sigmoid and bias: 20.7 us (33.7 with 64-bit
+// exchanges in every reduction and all experts in the last search); one token
+// without groups 4.9 us (9.9).
 template <int VPL>
 __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
 {
@@ -111,6 +112,7 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
     constexpr int kSlots = VPL * kWave + kMaxGroups;
     __shared__ double choice_lds[kGateWaves][kSlots];
     __shared__ double key_lds[kGateWaves][kSlots];
+    __shared__ float logit_lds[kGateWaves][kSlots];
     __shared__ uint8_t out_lds[kGateWaves][kSlots];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -165,10 +167,15 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
                 const int to = e + group_of(e);
                 choice_lds[wave][to] = c;
                 key_lds[wave][to] = key[i];
+                logit_lds[wave][to] = l[i];
                 out_lds[wave][to] = 1;
             }
         }
     }
+    double bk = kNone;      // this lane's best, its expert and its logit
+    int bi = kMaxExperts;
+    float bl = 0.f;
+    bool packed = false;    // the lane has that one candidate at most
     if (groups) {
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -215,21 +222,35 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
         }
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        // if the used groups' members fit the wave, one a lane: in the order of
+        // their groups, so of their ids
+        packed = a.topk_groups * per <= kWave;
+        if (packed) {
+            const int r = group_of(lane), j = lane - r * per;
+            int group = -1;
+            uint64_t left = used;
+            for (int q = 0; q < a.topk_groups && left != 0; ++q, left &= left - 1)
+                group = r == q ? (int)__builtin_ctzll(left) : group;
+            const int at = group >= 0 ? group * (per + 1) + j : 0;
+            const bool in = group >= 0 && (!a.limit || out_lds[wave][at] == 2);
+            const double k = key_lds[wave][at];
+            bk = in ? k : kNone;
+            bi = in ? group * per + j : kMaxExperts;
+            bl = logit_lds[wave][at];
+        } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = lane + kWave * i;
-            const int at = e < a.E ? e : 0, group = group_of(at);
-            const uint32_t keeps = (uint32_t)(used >> group) & (a.limit ? out_lds[wave][at + group] >> 1 : 1u);
-            key[i] = (keeps & 1u) != 0u ? key[i] : kNone;
+            for (int i = 0; i < VPL; ++i) {
+                const int e = lane + kWave * i;
+                const int at = e < a.E ? e : 0, group = group_of(at);
+                const uint32_t keeps = (uint32_t)(used >> group) & (a.limit ? out_lds[wave][at + group] >> 1 : 1u);
+                key[i] = (keeps & 1u) != 0u ? key[i] : kNone;
+            }
         }
     }
 
     // K times the best that is left; lane k keeps the k-th
     int my_id = -1;
     float my_l = 0.f;
-    double bk = kNone;      // this lane's best, its expert and its logit
-    int bi = kMaxExperts;
-    float bl = 0.f;
     auto local_best = [&] {
         bk = kNone;
         bi = kMaxExperts;
@@ -241,7 +262,7 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
             bl = more ? l[i] : bl;
         }
     };
-    local_best();
+    if (!packed) local_best();
     for (int k = 0; k < a.K; ++k) {
         const int from = wave_best(bk, bi);
         if (from < 0) break;
@@ -249,9 +270,13 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
         const float lv = lane_value(bl, from);
         my_id = lane == k ? id : my_id;
         my_l = lane == k ? lv : my_l;
+        if (packed) {
+            bk = lane == from ? kNone : bk;
+        } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) key[i] = lane + kWave * i == id ? kNone : key[i];
-        local_best();
+            for (int i = 0; i < VPL; ++i) key[i] = lane + kWave * i == id ? kNone : key[i];
+            local_best();
+        }
     }
     const bool live = my_id >= 0;
     double v = 0.0;

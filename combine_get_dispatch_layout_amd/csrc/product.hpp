@@ -921,7 +921,7 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
 // Latency bound: a block has few bytes (196 KB for one token, bf16, 2048 x
 // 768, top-8) and what counts is that they are asked for early.  One token
 // (GPU time of the layer): 27.7 us with the general kernel and k_layer_reduce,
-// 24.4 us with this one; MXFP4 20.6 and 16.5 us.
+// 24.9 us with this one; MXFP4 20.6 and 16.8 us.
 constexpr int kFewWaves = 16;
 constexpr int kFewTokens = 16;
 
@@ -1193,9 +1193,9 @@ hipError_t launch_kind(const ProductArgs& a, hipStream_t s)
         return kw;
     };
     // Few tiles (less than one a wave of the big blocks): blocks of four waves
-    // and short rings, three to a CU.  One token through the bf16 layer's up
-    // projection takes 14.6 us so and 17.8 us with the big blocks; a decode
-    // batch's (32768 tiles) 1374 and 667 us.
+    // and short rings, three to a CU.  At one and the same step of the kernel
+    // one token through the bf16 layer took 28.4 us so and 30.4 us with the big
+    // blocks alone; a decode batch (32768 tiles) 1374 us so and 816 us with them.
     constexpr int US = 2;
     if (tt == 1 && tiles < kAtOnce) {
         const int kw = waves_per_tile(4, US, 4 * kAtOnce);
