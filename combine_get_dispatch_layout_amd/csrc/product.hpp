@@ -28,10 +28,12 @@
 //   INT4:  32 columns; the four words of the four lanes of a row are
 //          transposed in registers (v_permlane16_swap, v_permlane32_swap), so
 //          that instruction j covers the 32 consecutive columns of lane j.
-//          Code q becomes the bf16 value 128 + q by an OR; a second
-//          instruction with the constant -(128 + zero) in B takes the offset
+//          Code q becomes the bf16 value 16 + q by an OR; a second
+//          instruction with the constant -(16 + zero) in B takes the offset
 //          away in fp32; the group's scale multiplies the fp32 sum, so no
-//          weight is rounded.  (Without the second instruction the 128-token
+//          weight is rounded.  16 is the smallest offset that leaves all codes
+//          one exponent: what the fp32 sums lose and the x at which they
+//          overflow go with it.  (Without the second instruction the 128-token
 //          layer would take 1153 us instead of 1314: the price of exact codes.)
 //
 // Measured on MI355X (GPU time): the up projection of a decode batch (128
@@ -143,12 +145,16 @@ constexpr int group_in_line(int v, int q)
     return KIND == kInt4G32 ? 2 * q + v : q;
 }
 
+// INT4: bf16 -(16 + zero) in both halves, for a zero byte and for 8.
+__device__ __forceinline__ uint32_t offset_of(uint32_t zero) { return (0xC180u | (zero & 15u) << 3) * 0x10001u; }
+constexpr uint32_t kOffset8 = 0xC1C0C1C0u;
+
 // What one span of a weight row multiplies with, from its scale words.
 template <int KIND>
 struct SpanScale {
     static constexpr int kGroups = Format<KIND>::kInt4 ? 4 / Format<KIND>::kGroupParts : 1;
     float s[kGroups];          // MXFP4: this lane's group alone
-    uint32_t off[kGroups];     // INT4: bf16 -(128 + zero), twice
+    uint32_t off[kGroups];     // INT4: bf16 -(16 + zero), twice
 };
 
 // Span v of the block's line ln.
@@ -167,9 +173,9 @@ __device__ __forceinline__ SpanScale<KIND> span_scale(const Scales<KIND, U>& b, 
             const int i = ln * (256 / Format<KIND>::kGroup) + group_in_line<KIND>(v, q);
             const uint32_t w = b.s[i / 2];
             o.s[q] = __uint_as_float(i % 2 ? w & 0xFFFF0000u : w << 16);
-            o.off[q] = 0xC308C308u;
-            if (zeros)      // bytes zero, 0xC3, zero, 0xC3
-                o.off[q] = __builtin_amdgcn_perm(b.z[i / 4], 0xC3C3C3C3u,
+            o.off[q] = kOffset8;
+            if (zeros)      // bytes 0x80 | zero << 3, 0xC1, and again
+                o.off[q] = __builtin_amdgcn_perm((b.z[i / 4] << 3 & 0x78787878u) | 0x80808080u, 0xC1C1C1C1u,
                                                  0x00040004u + (uint32_t)(i % 4) * 0x00010001u);
         }
     }
@@ -227,7 +233,8 @@ __device__ __forceinline__ void expand(u32x4 f, const SpanScale<KIND>& s, u32x4 
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) b[j][i] = ((q[j] >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+            for (int i = 0; i < 4; ++i)
+                b[j][i] = ((i ? q[j] >> (4 * i - 3) : q[j] << 3) & 0x00780078u) | 0x41804180u;
     }
 }
 
@@ -685,7 +692,7 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
                     const int gi = min(want, row_groups - 1);
                     const uint32_t w = reinterpret_cast<const uint16_t*>(a.w.scales)[base + gi];
                     o.s[q] = want == gi ? __uint_as_float(w << 16) : 0.f;
-                    o.off[q] = (0xC300u | (has_zeros ? a.w.zeros[base + gi] : 8u)) * 0x10001u;
+                    o.off[q] = has_zeros ? offset_of(a.w.zeros[base + gi]) : kOffset8;
                 }
             }
             return o;
@@ -978,7 +985,7 @@ __device__ __forceinline__ void load_line(const WeightArgs& w, int64_t row0, int
                 const int gi = min(want, row_groups - 1);
                 const uint32_t sc = reinterpret_cast<const uint16_t*>(w.scales)[base + gi];
                 o.s[v].s[q] = want == gi ? __uint_as_float(sc << 16) : 0.f;
-                o.s[v].off[q] = (0xC300u | (w.zeros ? w.zeros[base + gi] : 8u)) * 0x10001u;
+                o.s[v].off[q] = w.zeros ? offset_of(w.zeros[base + gi]) : kOffset8;
             }
         }
     }

@@ -95,7 +95,10 @@ enum {
     EP_WEIGHT_INT4 = 2     /* d_data two codes a byte as above; an element is
                               (code - zero) * scale, with d_scales bf16
                               [E, rows, cols/group] and d_zeros uint8 of that
-                              shape holding 0..15, or NULL: every zero is 8    */
+                              shape holding 0..15, or NULL: every zero is 8.
+                              Multiplied as (16 + code) - (16 + zero): no sum of
+                              a group overflows for |x| up to 2^116; an infinity
+                              in x makes NaN                                   */
 };
 
 /* Applied to a product's rows. */

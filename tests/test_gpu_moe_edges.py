@@ -1,0 +1,61 @@
+"""GPU tests of the router, the products and the expert layer where results can
+go wrong without a plain case showing it."""
+import numpy as np
+import pytest
+import torch
+
+import moe_reference as R
+from combine_get_dispatch_layout_amd import ep, moe
+
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+# ---- INT4: what the codes' offset costs -----------------------------------------
+
+def int4(codes, group, zero, scale):
+    """An INT4 stack of one matrix with one scale and one zero (None: 8)."""
+    M, C = codes.shape
+    data = torch.from_numpy((codes[:, ::2] | codes[:, 1::2] << 4).astype(np.uint8)).cuda()
+    s = torch.full((M, C // group), scale, dtype=torch.bfloat16, device="cuda")
+    z = None if zero is None else torch.full((M, C // group), zero, dtype=torch.uint8, device="cuda")
+    return moe.Weights(moe.EP_WEIGHT_INT4, data, s, z, group=group)
+
+
+@pytest.mark.parametrize("rows", [1, 9, 20])
+@pytest.mark.parametrize("zero", [None, 5, 0, 15])
+@pytest.mark.parametrize("group,C", [(32, 512), (32, 160), (64, 512), (64, 192), (128, 512), (128, 384)])
+def test_int4_large_columns_of_zero_weight(group, C, zero, rows):
+    """Each group has a column of x = 2^17 whose weight is 0; the others are
+    multiples of 1/4 up to 1.  With codes as 16 + q every partial sum is a
+    multiple of 1/4 of at most 31 * 2^17 + 31 * 127 < 2^22 (exact in fp32), so
+    y is the exact sum, rounded once."""
+    say(f"[int4 offset] {group} {C} {zero} {rows}")
+    rng = np.random.default_rng(C + rows)
+    M, z = 37, 8 if zero is None else zero
+    codes = rng.integers(0, 16, (M, C))
+    x = rng.integers(-4, 5, (rows, C)) / 4
+    big = np.arange(0, C, group) + rng.integers(0, group, C // group)
+    codes[:, big] = z
+    x[:, big] = 2.0 ** 17 * rng.choice([-1, 1], (rows, len(big)))
+    y = moe.ep_matvec(int4(codes, group, zero, 1.0), torch.from_numpy(x).to(torch.bfloat16).cuda())
+    want = torch.from_numpy(x @ (codes - z).T).float().to(torch.bfloat16)
+    assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_int4_x_near_the_largest(group, rows):
+    """One column of 2^121: (16 + q) x is at most 31 * 2^121 < 2^126, so the
+    product is exact; the other columns are zeros."""
+    rng = np.random.default_rng(group)
+    codes = rng.integers(0, 16, (33, 256))
+    for zero in (None, 0, 15):
+        x = torch.zeros((rows, 256), dtype=torch.bfloat16)
+        x[:, 77] = 2.0 ** 121
+        y = moe.ep_matvec(int4(codes, group, zero, 2.0 ** -20), x.cuda())
+        want = (codes[:, 77] - (8 if zero is None else zero)) * 2.0 ** 101
+        assert np.array_equal(y.double().cpu().numpy(), np.broadcast_to(want, (rows, 33)))
