@@ -19,6 +19,16 @@ constexpr int kGateWaves = 4;
 constexpr int kMaxGroups = 64;
 constexpr double kNone = -__builtin_huge_val();
 
+// Blocks of one row of the grid, which holds fewer than 2^32 threads: 2^26
+// tokens and more take several rows.
+constexpr int64_t kGridRow = 1 << 20;
+
+// The block's first token.
+__device__ __forceinline__ int64_t first_token()
+{
+    return ((int64_t)blockIdx.y * kGridRow + blockIdx.x) * kGateWaves;
+}
+
 __device__ __forceinline__ float load_logit(const void* p, bool bf16, int64_t i)
 {
     if (bf16) return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << 16);
@@ -116,7 +126,7 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
     __shared__ uint8_t out_lds[kGateWaves][kSlots];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t t = (int64_t)blockIdx.x * kGateWaves + wave;
+    const int64_t t = first_token() + wave;
     if (t >= a.N) return;
     int32_t* const idx = a.idx + t * a.K;
     float* const w = a.w + t * a.K;
@@ -320,7 +330,7 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate_backward(GateArgs a)
 {
     constexpr int V = VPL < 4 ? VPL : 4;            // neighbours in a lane
     const int lane = threadIdx.x & (kWave - 1);
-    const int64_t t = (int64_t)blockIdx.x * kGateWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t t = first_token() + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (t >= a.N) return;
     const int64_t base = t * a.E;
     const float kLow = -__builtin_huge_valf();
@@ -417,7 +427,8 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate_backward(GateArgs a)
 template <bool BACK, int VPL>
 hipError_t launch_vpl(const GateArgs& a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.N + kGateWaves - 1) / kGateWaves)), block(kGateWaves * kWave);
+    const int64_t blocks = (a.N + kGateWaves - 1) / kGateWaves, row = blocks < kGridRow ? blocks : kGridRow;
+    const dim3 grid((unsigned)row, (unsigned)((blocks + row - 1) / row)), block(kGateWaves * kWave);
     if constexpr (BACK) hipLaunchKernelGGL(k_gate_backward<VPL>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(k_gate<VPL>, grid, block, 0, s, a);
     return hipGetLastError();

@@ -59,3 +59,25 @@ def test_int4_x_near_the_largest(group, rows):
         y = moe.ep_matvec(int4(codes, group, zero, 2.0 ** -20), x.cuda())
         want = (codes[:, 77] - (8 if zero is None else zero)) * 2.0 ** 101
         assert np.array_equal(y.double().cpu().numpy(), np.broadcast_to(want, (rows, 33)))
+
+
+# ---- router: batches whose threads pass 32 bits ------------------------------------
+
+def test_gate_of_more_threads_than_32_bits():
+    """2^26 tokens at one wave each are 2^32 threads."""
+    N = (1 << 26) + 5
+    lg = torch.randint(-2, 3, (N, 2), dtype=torch.int8, device="cuda").to(torch.bfloat16)
+    cfg = moe.GateConfig(2, 1, moe.EP_SCORE_SIGMOID, renormalize=False, scale=4.0)
+    idx, w = moe.ep_gate(cfg, lg)
+    second = lg[:, 1] > lg[:, 0]
+    assert torch.equal(idx[:, 0], second.int())
+    top = torch.where(second, lg[:, 1], lg[:, 0]).float()
+    # the five logits' weights: sigmoids rounded once
+    for v in range(-2, 3):
+        got = w[:, 0][top == v]
+        assert got.numel() == 0 or (got.min() == got.max() and
+                                    abs(float(got[0]) / 4 * (1 + np.exp(-v)) - 1) <= 2 * R.F32_HALF)
+    del w, top
+    grad = moe.ep_gate_backward(cfg, lg, idx, torch.ones((N, 1), device="cuda"))
+    assert torch.equal(grad != 0, torch.stack((~second, second), 1))
+    assert (grad[-5:].float().sum(1) > 0).all()
