@@ -31,7 +31,7 @@ thread_local char g_msg[512] = "";
 #define EP_FAIL(st, ...) epk::host_fail((st), __FILE__, __LINE__, __VA_ARGS__)
 #define EP_HIP(call)                                                                          \
     do {                                                                                      \
-        hipError_t e_ = (call);                                                               \
+        hipError_t e_ = epk::with_refusal(call);                                              \
         if (e_ != hipSuccess) return EP_FAIL(EP_ERR_HIP, "%s: %s", #call, hipGetErrorString(e_)); \
     } while (0)
 

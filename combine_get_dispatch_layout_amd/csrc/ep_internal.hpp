@@ -148,12 +148,28 @@ struct LaunchEvents {
     hipEvent_t stop = nullptr;
 };
 
-// Launches `kernel`; with events it goes through hipExtLaunchKernelGGL so the
-// events take the kernel's own start / end timestamps.
+// Set where launch_k refused a launch, until the host side asks.
+inline thread_local bool launch_refused = false;
+
+inline hipError_t with_refusal(hipError_t e)
+{
+    const bool refused = launch_refused;
+    launch_refused = false;
+    return e == hipSuccess && refused ? hipErrorInvalidConfiguration : e;
+}
+
+// Launches `kernel`, unless a row of the grid would have 2^32 threads or more:
+// such a launch would be cut short without an error.  With events it goes
+// through hipExtLaunchKernelGGL so the events take the kernel's own start /
+// end timestamps.
 template <typename K, typename... Args>
 inline void launch_k(K kernel, dim3 grid, dim3 block, size_t lds, hipStream_t s, hipEvent_t start,
                      hipEvent_t stop, Args... args)
 {
+    if ((uint64_t)grid.x * block.x >= (uint64_t)1 << 32) {
+        launch_refused = true;
+        return;
+    }
     if (start != nullptr || stop != nullptr)
         hipExtLaunchKernelGGL(kernel, grid, block, (uint32_t)lds, s, start, stop, 0u, args...);
     else

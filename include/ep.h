@@ -267,7 +267,10 @@ ep_status ep_get_layout(ep_handle* h, const int32_t* d_topk_idx, int64_t num_tok
  *     group holding an infinity or NaN gets unspecified codes and scale.
  *   Reusing a handle across calls is cached dispatch ([P3] §3.2).
  *   EP_ERR_CAPACITY if S is known on the host and exceeds the capacity;
- *   otherwise rows beyond it are skipped and flagged on the device. */
+ *   otherwise rows beyond it are skipped and flagged on the device.
+ *   A launch has a wave for each token and chunk of its row (64 to 256 vectors
+ *   of 8 elements): 2^26 of them and more are refused here and in the calls
+ *   below (EP_ERR_HIP, invalid configuration); such a batch goes in ranges. */
 ep_status ep_dispatch(const ep_handle* h, const void* d_x, int64_t token_begin, int64_t token_end,
                       void* d_recv_x, void* d_recv_scales, int64_t recv_capacity_rows,
                       void* stream);

@@ -81,3 +81,22 @@ def test_gate_of_more_threads_than_32_bits():
     grad = moe.ep_gate_backward(cfg, lg, idx, torch.ones((N, 1), device="cuda"))
     assert torch.equal(grad != 0, torch.stack((~second, second), 1))
     assert (grad[-5:].float().sum(1) > 0).all()
+
+
+def test_shuffle_of_more_threads_than_32_bits():
+    """2^26 rows of one wave each: refused as one launch, right in two ranges."""
+    N = (1 << 26) + 320
+    cfg = ep.Config(hidden=8, num_topk=1, num_experts=1, num_ranks=1)
+    h = ep.ep_handle_init(cfg, N)
+    ep.ep_get_layout(h, torch.zeros((N, 1), dtype=torch.int32, device="cuda"), alloc_outputs=False)
+    x = torch.randint(-9, 9, (N, 8), dtype=torch.int8, device="cuda").to(torch.bfloat16)
+    recv = torch.full_like(x, 77)
+    out = torch.full_like(x, 77)
+    for call in (lambda **kw: ep.ep_dispatch(h, x, recv, **kw), lambda **kw: ep.ep_combine(h, recv, None, out, **kw)):
+        with pytest.raises(ep.EpError) as ei:
+            call()
+        assert ei.value.status == ep.EP_ERR_HIP and "configuration" in str(ei.value)
+        call(token_begin=0, token_end=N // 2)
+        call(token_begin=N // 2, token_end=N)
+    assert torch.equal(recv, x) and torch.equal(out, x)
+    assert ep.ep_check_error(h) == (ep.EP_OK, 0)
