@@ -77,6 +77,13 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Orders one lane's writes to LDS before another's reads in the same wave.
+__device__ __forceinline__ void wave_exchange()
+{
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // Weights and scales are read through a buffer resource per tile (its first
 // row as the base, its rows as the bound): the address of a load is one lane
 // offset that never changes and one scalar, so the loop has no address
@@ -545,7 +552,9 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
             ++segments;
         }
         const uint32_t batch_stop = min(stop, (uint32_t)(pass0 + segments) * (uint32_t)tiles);
+        // the lists: of several waves, or the same from every wave for itself
         if (kPairs && !few) lds_barrier();
+        else wave_exchange();
 
         // ---- loads: where the next block comes from
         Buffer data[RT], scales[RT], zeros[RT];
