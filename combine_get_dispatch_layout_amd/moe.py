@@ -3,7 +3,8 @@ expert weights, whole expert layer), over torch tensors.
 
 As in ep.py: argument marshalling only, the functions carry the C names, the
 work is queued on the current stream of the tensors' device, and outputs are
-allocated with torch when none are passed.
+allocated with torch when none are passed.  ep_gate alone takes part in
+autograd; the other calls' outputs have no gradient.
 """
 import ctypes
 from dataclasses import dataclass, field
@@ -77,7 +78,8 @@ def _ptr(t):
 
 def _call(device, fn, *args):
     """fn(*args, stream) on the device's current stream, with the device
-    current."""
+    current.  (By torch's internal names: torch.cuda.current_stream alone takes
+    1.9 us of a call's 9.)"""
     index = device.index
     if torch._C._cuda_getDevice() == index:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
@@ -123,12 +125,46 @@ def _check_logits(cfg, logits):
     return logits.shape[0], logits.device
 
 
+class _Gate(torch.autograd.Function):
+    """ep_gate with ep_gate_backward as its weights' gradient."""
+
+    @staticmethod
+    def forward(ctx, cfg, logits, bias, token_mask):
+        topk_idx, topk_weights = ep_gate(cfg, logits, bias, token_mask)
+        ctx.cfg = cfg
+        ctx.save_for_backward(logits, topk_idx)
+        ctx.mark_non_differentiable(topk_idx)
+        ctx.set_materialize_grads(False)
+        return topk_idx, topk_weights
+
+    @staticmethod
+    def backward(ctx, _, grad_weights):
+        if grad_weights is None:
+            return None, None, None, None
+        if torch.is_grad_enabled():     # create_graph: would lose the second order silently
+            raise RuntimeError("ep_gate has a first order gradient only")
+        logits, topk_idx = ctx.saved_tensors
+        return None, ep_gate_backward(ctx.cfg, logits, topk_idx, grad_weights.contiguous()), None, None
+
+
 def ep_gate(cfg: GateConfig, logits: torch.Tensor, bias: Optional[torch.Tensor] = None,
             token_mask: Optional[torch.Tensor] = None, topk_idx: Optional[torch.Tensor] = None,
             topk_weights: Optional[torch.Tensor] = None):
     """Chooses num_topk experts per row of logits [N, E] (fp32 or bf16).  bias
     fp32 [E] acts on the choice only; token_mask bool / uint8 [N]: rows with 0
-    get none.  Returns (topk_idx int32 [N,K], topk_weights fp32 [N,K])."""
+    get none.  Returns (topk_idx int32 [N,K], topk_weights fp32 [N,K]).  Where
+    autograd records and the logits require a gradient, the weights have one
+    (the choice held fixed); both outputs are then allocated here, and leaf
+    logits are refused inside a graph capture."""
+    if logits.requires_grad and torch.is_grad_enabled():
+        if topk_idx is not None or topk_weights is not None:
+            raise ValueError("topk_idx and topk_weights must be left out where the logits require a gradient")
+        # a leaf's gradient accumulates on the stream of its first use, which a
+        # backward pass in the capture must not touch
+        if logits.is_leaf and logits.is_cuda and torch.cuda.is_current_stream_capturing():
+            raise ValueError("leaf logits that require a gradient must not be used in a graph capture: "
+                             "capture ep_gate (without autograd) and ep_gate_backward")
+        return _Gate.apply(cfg, logits, bias, token_mask)
     N, dev = _check_logits(cfg, logits)
     shape = (N, cfg.num_topk)
     if topk_idx is None:

@@ -100,3 +100,89 @@ def test_shuffle_of_more_threads_than_32_bits():
         call(token_begin=N // 2, token_end=N)
     assert torch.equal(recv, x) and torch.equal(out, x)
     assert ep.ep_check_error(h) == (ep.EP_OK, 0)
+
+
+# ---- router: the weights' gradient through autograd ----------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+def test_gate_weights_have_the_gradient(score, renorm, dtype):
+    N, E, K = 19, 40, 4
+    cfg = moe.GateConfig(E, K, dict(softmax=0, sigmoid=1)[score], renorm, scale=2.5)
+    g = torch.Generator().manual_seed(4)
+    lg = torch.randn((N, E), generator=g).to(dtype).cuda().requires_grad_()
+    gw = torch.randn((N, K), generator=g).cuda()
+    mask = (torch.arange(N) % 5 != 0).cuda()
+    bias = torch.randn(E, generator=g).cuda()
+    idx, w = moe.ep_gate(cfg, lg, bias, mask)
+    assert w.requires_grad and not idx.requires_grad
+    with torch.no_grad():
+        ridx, rw = moe.ep_gate(cfg, lg, bias, mask)
+    assert torch.equal(idx, ridx) and torch.equal(w, rw) and not rw.requires_grad
+    want = moe.ep_gate_backward(cfg, lg.detach(), idx, gw)
+    assert (want[mask] != 0).any(1).all() and (want[~mask] == 0).all()
+    w.backward(gw)
+    assert lg.grad.dtype == dtype and torch.equal(lg.grad, want)
+    # a gradient that is a broadcast scalar; a second use adds up
+    lg.grad = None
+    _, w = moe.ep_gate(cfg, lg, bias, mask)
+    (w.sum() + (w * gw).sum()).backward()
+    assert torch.equal(lg.grad, moe.ep_gate_backward(cfg, lg.detach(), idx, 1 + gw))
+    # through what made the logits
+    x, r = torch.randn((N, 8), generator=g).cuda(), torch.randn((8, E), generator=g).cuda().requires_grad_()
+    z = x @ r
+    _, w = moe.ep_gate(cfg, z, bias)
+    w.backward(gw)
+    with torch.no_grad():
+        i, _ = moe.ep_gate(cfg, z, bias)
+        assert torch.equal(r.grad, x.t() @ moe.ep_gate_backward(cfg, z.detach(), i, gw))
+
+
+def test_gate_gradient_refuses_given_outputs_and_second_order():
+    cfg = moe.GateConfig(8, 2)
+    lg = torch.randn((3, 8), device="cuda", requires_grad=True)
+    with pytest.raises(ValueError, match="left out"):
+        moe.ep_gate(cfg, lg, topk_idx=torch.empty((3, 2), dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="left out"):
+        moe.ep_gate(cfg, lg, topk_weights=torch.empty((3, 2), device="cuda"))
+    _, w = moe.ep_gate(cfg, lg)
+    with pytest.raises(RuntimeError, match="first order"):
+        torch.autograd.grad(w[:, 0].sum(), lg, create_graph=True)
+    idx, w = moe.ep_gate(cfg, lg)
+    idx.zero_()                                     # the choice was overwritten
+    with pytest.raises(RuntimeError, match="inplace"):
+        w.sum().backward()
+    with pytest.MonkeyPatch.context() as mp:        # as inside a capture
+        mp.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        with pytest.raises(ValueError, match="capture"):
+            moe.ep_gate(cfg, lg)
+    empty = torch.zeros((0, 8), device="cuda", requires_grad=True)
+    moe.ep_gate(cfg, empty)[1].sum().backward()
+    assert empty.grad.shape == (0, 8)
+
+
+def test_gate_graph_replays():
+    """A captured choice and gradient against the eager ones."""
+    cfg = moe.GateConfig(64, 6, moe.EP_SCORE_SIGMOID, num_groups=8, topk_groups=3, group_top=2)
+    lg, gw = torch.randn((50, 64), device="cuda"), torch.randn((50, 6), device="cuda")
+    out = [torch.empty((50, 6), dtype=torch.int32, device="cuda"), torch.empty((50, 6), device="cuda"), torch.empty_like(lg)]
+
+    def step():
+        moe.ep_gate(cfg, lg, topk_idx=out[0], topk_weights=out[1])
+        moe.ep_gate_backward(cfg, lg, out[0], gw, out[2])
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        lg.normal_()
+        gw.normal_()
+        for t in out:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        idx, w = moe.ep_gate(cfg, lg)
+        assert torch.equal(out[0], idx) and torch.equal(out[1], w)
+        assert torch.equal(out[2], moe.ep_gate_backward(cfg, lg, idx, gw))
