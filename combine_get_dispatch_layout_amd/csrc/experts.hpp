@@ -3,14 +3,12 @@
 #pragma once
 
 #include "ep_internal.hpp"
+#include "product_shape.hpp"
 
 namespace epk {
 
 // Pairs (token, k) of one whole-layer call: 256 tokens x 16.
 constexpr int kMaxPairs = 4096;
-
-// Storage formats as the kernels are instantiated for them.
-enum WeightKind { kBf16 = 0, kMxfp4 = 1, kInt4G32 = 2, kInt4G64 = 3, kInt4G128 = 4 };
 
 struct WeightArgs {
     const uint8_t* data;

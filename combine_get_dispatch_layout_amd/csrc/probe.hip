@@ -6,6 +6,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "ep_moe.h"
+#include "product_shape.hpp"
+
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -199,4 +202,29 @@ extern "C" int ep_probe_stream(int mode, const void* d_src, void* d_dst, int64_t
         default: e = launch_m<EP_PROBE_COPY>(vpl, nontemporal, s, d, nvec, blocks, threads, hs); break;
     }
     return e == hipSuccess ? 0 : (int)e;
+}
+
+namespace {
+
+int weight_kind(int format, int group)
+{
+    if (format == EP_WEIGHT_BF16) return epk::kBf16;
+    if (format == EP_WEIGHT_MXFP4) return epk::kMxfp4;
+    return group == 32 ? epk::kInt4G32 : group == 64 ? epk::kInt4G64 : epk::kInt4G128;
+}
+
+}  // namespace
+
+extern "C" int ep_probe_product_path(int format, int group, int gate, int terms, int64_t cols, int64_t units,
+                                     int64_t experts, int64_t rows, int64_t* rows_at_once)
+{
+    const epk::prod::Shape s =
+        epk::prod::choose_shape(weight_kind(format, group), gate != 0, terms, cols, units, experts, rows);
+    if (rows_at_once) *rows_at_once = s.rows;
+    return s.path;
+}
+
+extern "C" int ep_probe_layer_in_two(int format, int group, int64_t tokens, int64_t topk, int64_t inter)
+{
+    return epk::prod::few_fits(weight_kind(format, group), tokens, tokens * topk, inter) ? 1 : 0;
 }

@@ -108,7 +108,7 @@ __device__ __forceinline__ u32x4 load_weights(Buffer b, uint32_t lane_off, uint3
 template <int KIND>
 struct Format {
     static constexpr bool kInt4 = KIND >= kInt4G32;
-    static constexpr int kLine = KIND == kBf16 ? 64 : 256;      // columns of a line
+    static constexpr int kLine = line_columns(KIND);
     static constexpr int kParts = KIND == kBf16 ? 1 : 4;        // instructions of a span
     static constexpr int kGroup = KIND == kInt4G128 ? 128 : KIND == kInt4G64 ? 64 : 32;
     // INT4: parts of a span that share a scale
@@ -512,7 +512,7 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
     // lines whose scales are loaded a block at a time, as whole words
     const int quick = row_groups % 4 == 0 ? full : 0;
     const int cols_up = (a.w.cols + F::kLine - 1) / F::kLine * F::kLine;
-    const int stride = cols_up * 2 + 16;             // of x in LDS; 16: rows start in different banks
+    const int stride = (int)x_stride(KIND, a.w.cols);           // of x in LDS
 
     while (at < stop) {
         // ---- a batch: tiles [at, batch_stop) of passes pass0, pass0 + 1, ...
@@ -938,9 +938,6 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
 // 768, top-8) and what counts is that they are asked for early.  One token
 // (GPU time of the layer): 27.7 us with the general kernel and k_layer_reduce,
 // 24.9 us with this one; MXFP4 20.6 and 16.8 us.
-constexpr int kFewWaves = 16;
-constexpr int kFewTokens = 16;
-
 // The lane's pair: its group's key, expert + kMaxExperts * (how often the
 // token listed it before), so that a group has each token once; -1: none.
 __device__ __forceinline__ int few_key(const ProductArgs& a, int e)
@@ -1011,7 +1008,7 @@ __global__ __launch_bounds__(kFewWaves* kWave, 4) void k_down_few(ProductArgs a)
     const int n = lane & 15, c = lane >> 4;
     const int row_bytes = (int)a.w.row_bytes;
     const int cols_up = (a.w.cols + F::kLine - 1) / F::kLine * F::kLine;
-    const int stride = cols_up * 2 + 16;
+    const int stride = (int)x_stride(KIND, a.w.cols);
     const int lo_bytes = a.P * stride;
 
     int e = lane < a.P ? a.topk[lane] : -1;
@@ -1102,24 +1099,15 @@ __global__ __launch_bounds__(kFewWaves* kWave, 4) void k_down_few(ProductArgs a)
             reinterpret_cast<uint16_t*>(a.y)[(int64_t)(4 * c + i) * a.ldy + tile0 + n] = to_bf16(sum[i]);
 }
 
-// LDS of k_down_few.
-template <int KIND>
-int64_t few_bytes(const ProductArgs& a)
-{
-    using F = Format<KIND>;
-    const int64_t stride = ((int64_t)a.w.cols + F::kLine - 1) / F::kLine * F::kLine * 2 + 16;
-    const int64_t x = 2 * (int64_t)a.P * stride, red = (int64_t)kFewWaves * kWave * 16;
-    return x > red ? x : red;
-}
-
 // The down projection and the sum over experts in one kernel, if the batch is
 // a handful (*done); the caller takes the general path otherwise.
 template <int KIND>
 hipError_t launch_down_few(const ProductArgs& a, bool* done, hipStream_t s)
 {
-    const int64_t lds = few_bytes<KIND>(a);
-    *done = a.P <= kWave && a.P / a.K <= kFewTokens && lds <= 65536;
+    static_assert(kFewPairs == kWave, "a pair a lane");
+    *done = few_fits(KIND, a.P / a.K, a.P, a.w.cols);
     if (!*done) return hipSuccess;
+    const int64_t lds = few_bytes(KIND, a.P, a.w.cols);
     if (lds > 32768)
         (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_down_few<KIND>),
                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -1141,36 +1129,24 @@ inline int num_cus()
     return n;
 }
 
-// Dynamic LDS of a block, at most (its static arrays take 13 KB of the CU's
-// 160 KB).
-constexpr int64_t kLdsRoom = 131072;
-
-// LDS in which the waves of a team add their sums: two buffers.
-constexpr int64_t sums_bytes(int waves, int kw, int tt)
-{
-    return kw > 1 ? 2 * (int64_t)waves * 2 * tt * kWave * 16 : 0;
-}
-
 template <int KIND, int EPI, int TT, bool DIRECT, int U, int kWaves>
-hipError_t launch_shape(ProductArgs a, int64_t room, int kw, int64_t rows, int64_t max_rows, int64_t tiles,
-                        hipStream_t s)
+hipError_t launch_shape(ProductArgs a, const Shape& c, int64_t max_rows, hipStream_t s)
 {
-    using F = Format<KIND>;
     constexpr int kPlanes = EPI == kStoreF32 ? 2 : 1;
-    a.kw = kw;
-    a.pass_rows = (int)rows;
-    a.pass_magic = div_magic((uint32_t)rows);
-    a.dense_passes = (int)((a.num_rows + rows - 1) / rows);
-    const int64_t stride = ((int64_t)a.w.cols + F::kLine - 1) / F::kLine * F::kLine * 2 + 16;
+    a.kw = c.kw;
+    a.pass_rows = (int)c.rows;
+    a.pass_magic = div_magic((uint32_t)c.rows);
+    a.dense_passes = (int)((a.num_rows + c.rows - 1) / c.rows);
+    const int64_t stride = x_stride(KIND, a.w.cols), sums = sums_bytes(kWaves, c.kw, TT);
     // rows of several passes go to LDS together, as many as there is room for
-    int64_t x_rows = DIRECT ? kListRows : (room - sums_bytes(kWaves, kw, TT)) / (kPlanes * stride);
+    int64_t x_rows = DIRECT ? kListRows : (c.room - sums) / (kPlanes * stride);
     x_rows = x_rows < max_rows ? x_rows : max_rows;
     a.x_rows = (int)(x_rows < kListRows ? x_rows : kListRows);
     a.x_bytes = DIRECT ? 0 : (int)(a.x_rows * kPlanes * stride);
-    const int64_t lds = a.x_bytes + sums_bytes(kWaves, kw, TT);
+    const int64_t lds = a.x_bytes + sums;
     if (lds > kLdsRoom) return hipErrorInvalidValue;
     const int64_t most = kWaves == 4 && TT == 1 ? 1 << 30 : (int64_t)num_cus();
-    const int64_t need = (tiles + kWaves / kw - 1) / (kWaves / kw);
+    const int64_t need = (c.tiles + kWaves / c.kw - 1) / (kWaves / c.kw);
     const dim3 grid((unsigned)(need < most ? need : most));
     if (lds > 32768)
         (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_product<KIND, EPI, TT, DIRECT, U, kWaves>),
@@ -1179,56 +1155,22 @@ hipError_t launch_shape(ProductArgs a, int64_t room, int kw, int64_t rows, int64
     return hipGetLastError();
 }
 
-// Waves of the big blocks (one of eight waves a CU) that run at a time.
-constexpr int64_t kAtOnce = 2048;
-
 // One kernel for the whole product.
 template <int KIND, int EPI>
 hipError_t launch_kind(const ProductArgs& a, hipStream_t s)
 {
-    using F = Format<KIND>;
     constexpr bool kPairs = EPI == kSwigluSplit || EPI == kStoreF32;
     constexpr bool kGate = EPI == kSwigluBf16 || EPI == kSwigluSplit;
-    constexpr int kPlanes = EPI == kStoreF32 ? 2 : 1;
-    // spans of a block (2 where x or the scales take more registers)
-    constexpr int U = KIND == kInt4G32 ? 2 : 4, UD = KIND == kBf16 ? 4 : 2;
-    const int64_t max_rows = kPairs || a.count ? a.P : a.num_rows;
-    if (max_rows <= 0) return hipSuccess;
-    const int64_t experts = kPairs || a.count ? (max_rows < a.E ? max_rows : a.E) : 1;
-    const int64_t likely = (max_rows + experts - 1) / experts;     // rows of an expert
-    const int tt = likely > 16 ? 2 : 1;
-    // tiles of all experts' passes, if their rows are spread evenly
-    const int64_t passes = experts * ((likely + 16 * tt - 1) / (16 * tt));
-    const int64_t tiles = passes * ((a.units + (kGate ? 15 : 31)) / (kGate ? 16 : 32));
-    const int64_t stride = ((int64_t)a.w.cols + F::kLine - 1) / F::kLine * F::kLine * 2 + 16;
-    // waves of a team: as long as all waves' work fits the GPU at once
-    auto waves_per_tile = [&](int most, int u, int64_t at_once) {
-        const int64_t blocks = (a.w.row_bytes / 64 + u - 1) / u;
-        int kw = 1;
-        while (kw < most && kw * 2 <= blocks && tiles * kw * 2 <= at_once) kw *= 2;
-        return kw;
-    };
-    // Few tiles (less than one a wave of the big blocks): blocks of four waves
-    // and short rings, three to a CU.  At one and the same step of the kernel
-    // one token through the bf16 layer took 28.4 us so and 30.4 us with the big
-    // blocks alone; a decode batch (32768 tiles) 1374 us so and 816 us with them.
-    constexpr int US = 2;
-    if (tt == 1 && tiles < kAtOnce) {
-        const int kw = waves_per_tile(4, US, 4 * kAtOnce);
-        const int64_t fit = (65536 - sums_bytes(4, kw, 1)) / (kPlanes * stride);
-        if (fit >= likely)
-            return launch_shape<KIND, EPI, 1, false, US, 4>(a, 65536, kw, fit < 16 ? fit : 16, max_rows, tiles, s);
+    const bool grouped = kPairs || a.count != nullptr;
+    const int64_t rows = grouped ? a.P : a.num_rows;
+    const Shape c = choose_shape(KIND, kGate, EPI == kStoreF32 ? 2 : 1, a.w.cols, a.units, grouped ? a.E : 1, rows);
+    switch (c.path) {
+        case kPathNone: return hipSuccess;
+        case kPathSmall: return launch_shape<KIND, EPI, 1, false, kSpansSmall, 4>(a, c, rows, s);
+        case kPathOneTile: return launch_shape<KIND, EPI, 1, false, spans_ahead(KIND, false), 8>(a, c, rows, s);
+        case kPathMemory: return launch_shape<KIND, EPI, 1, true, spans_ahead(KIND, true), 8>(a, c, rows, s);
+        default: return launch_shape<KIND, EPI, 2, false, spans_ahead(KIND, false), two_tile_waves(KIND)>(a, c, rows, s);
     }
-    const int kw = waves_per_tile(8, U, kAtOnce);
-    const int64_t fit = (kLdsRoom - sums_bytes(8, kw, tt)) / (kPlanes * stride);     // rows of x in LDS
-    if (fit < (likely < 16 ? likely : 16))
-        return launch_shape<KIND, EPI, 1, true, UD, 8>(a, kLdsRoom, kw, 16, max_rows, tiles, s);
-    if (tt == 1)
-        return launch_shape<KIND, EPI, 1, false, U, 8>(a, kLdsRoom, kw, fit < 16 ? fit : 16, max_rows, tiles, s);
-    // INT4 with two row tiles needs more than the 256 registers of eight waves
-    constexpr int W2 = F::kInt4 ? 4 : 8;
-    return launch_shape<KIND, EPI, 2, false, U, W2>(a, kLdsRoom, kw < W2 ? kw : W2, fit < 32 ? fit : 32, max_rows,
-                                                    tiles, s);
 }
 
 template <int KIND>

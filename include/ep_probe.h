@@ -1,9 +1,10 @@
 /*
  * ep_probe.h -- C ABI of libep_probe.so: streaming HBM probes that measure
  * the bandwidth a kernel can reach on this GPU for plain reads, writes and
- * copies.  They give the achievable ceilings the shuffle's kernels are
- * compared against (next to the published 8 TB/s peak): dispatch is bound
- * by HBM writes, combine by HBM reads.  Not part of the shuffle itself.
+ * copies, and, at the end, which kernel serves an expert product.  The probes
+ * give the achievable ceilings the shuffle's kernels are compared against
+ * (next to the published 8 TB/s peak): dispatch is bound by HBM writes,
+ * combine by HBM reads.  Not part of the shuffle itself.
  *
  * The shuffle's own measurement on the pages is bandwidth in GB/s per
  * stage ("DeepEP V1 vs V2 深度对比分析" §4.3); these probes fix what GB/s one
@@ -52,6 +53,26 @@ enum { EP_PROBE_GATHER = 3, EP_PROBE_SCATTER = 4 };
 int ep_probe_rows(int mode, const void* d_src, void* d_dst, const int32_t* d_slot,
                   int64_t num_tokens, int topk, int64_t row_bytes, int threads, int vec_per_lane,
                   void* stream);
+
+/* Which kernel serves a product of ep_moe.h, and how many rows of an expert it
+ * multiplies for one reading of the weights (*rows_at_once, or NULL); host
+ * arithmetic only.  format, group: of the weights; gate: 1 with EP_ACT_SWIGLU;
+ * terms: 1, or 2 for a layer's down projection; units: outputs after the
+ * activation; experts: 1 for ep_matvec; rows: num_rows, or num_tokens *
+ * num_topk of the layout or layer. */
+enum {
+    EP_PATH_NONE = 0,       /* no rows                                         */
+    EP_PATH_SMALL = 1,      /* fewer tiles than waves: blocks of four waves    */
+    EP_PATH_ONE_TILE = 2,   /* up to 16 rows at once, x in LDS                 */
+    EP_PATH_MEMORY = 3,     /* the same, x does not fit LDS                    */
+    EP_PATH_TWO_TILES = 4   /* up to 32 rows at once                           */
+};
+int ep_probe_product_path(int format, int group, int gate, int terms, int64_t cols, int64_t units,
+                          int64_t experts, int64_t rows, int64_t* rows_at_once);
+
+/* 1 if ep_moe_layer adds a token's experts inside the down projection (two
+ * kernels), 0 if it takes three; format, group: w_down's. */
+int ep_probe_layer_in_two(int format, int group, int64_t tokens, int64_t topk, int64_t inter);
 
 #ifdef __cplusplus
 }
