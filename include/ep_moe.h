@@ -129,8 +129,9 @@ typedef struct ep_weights {
 /* y = act(x W^T) for num_rows rows and one matrix (num_experts == 1):
  *   d_x bf16 [num_rows, cols], 16-byte aligned; d_y bf16 [num_rows, M] (or
  *   [num_rows, M/2] with EP_ACT_SWIGLU), not overlapping x.  Sums in fp32, one
- *   rounding to bf16.  Made for few rows: the weights are read once per pass of
- *   up to 16 rows (32 where there are more); num_rows * M below 2^35. */
+ *   rounding to bf16.  Made for few rows: up to 16 take one reading of the
+ *   weights, more one per 16 to 32 (what LDS holds of x; ep_probe_product_path
+ *   tells); num_rows * M below 2^35. */
 ep_status ep_matvec(const ep_weights* w, const void* d_x, int64_t num_rows, int32_t activation,
                     void* d_y, void* stream);
 
@@ -140,10 +141,15 @@ ep_status ep_matvec(const ep_weights* w, const void* d_x, int64_t num_rows, int3
  *   earlier product's y), d_y bf16 [x_rows, M or M/2].  Rows that hold no token
  *   (alignment padding, unfilled capacity, rows behind the last segment) are
  *   neither read nor written.  Rows at or beyond x_rows are skipped and flagged
- *   EP_FLAG_RECV_CAPACITY (ep_check_error); x_rows * M below 2^35.  Per expert
- *   passes of rows as in ep_matvec.  w->num_experts is the handle's;
- *   the handle has a finished layout (EP_ERR_STATE) in the expand form
- *   (EP_ERR_INVALID_ARG for non_expand, whose rows belong to ranks). */
+ *   EP_FLAG_RECV_CAPACITY (ep_check_error); x_rows * M below 2^35.
+ *   Made for decode batches: an expert's weights are read once per pass of its
+ *   rows, and a pass holds at least the mean of rows an expert or 16, at most 16
+ *   (32 where the mean is above 16).  With x so wide that LDS holds little more
+ *   than the mean, experts above it are read again; a prompt's rows are right,
+ *   at one reading per 16 to 32 of them.
+ *   w->num_experts is the handle's; the handle has a finished layout
+ *   (EP_ERR_STATE) in the expand form (EP_ERR_INVALID_ARG for non_expand, whose
+ *   rows belong to ranks). */
 ep_status ep_expert_matvec(const ep_handle* h, const ep_weights* w, const void* d_x,
                            int64_t x_rows, int32_t activation, void* d_y, void* stream);
 
@@ -154,8 +160,8 @@ ep_status ep_moe_workspace_size(const ep_handle* h, const ep_weights* w_up,
 /* The whole expert layer of num_tokens <= EP_MOE_MAX_TOKENS tokens:
  *   a[t,k] = silu(g) * u with (g, u) = W_up[idx[t,k]] x[t]
  *   out[t] = bf16( sum over k of w[t,k] * W_down[idx[t,k]] a[t,k] )
- * with a and every sum held in at least 16 bits of mantissa up to the one
- * rounding of out (ep_expert_matvec and ep_combine round a and each expert's
+ * with sums in fp32, a in 16 bits of mantissa (two bf16 terms) and one rounding
+ * of out (ep_expert_matvec and ep_combine round a and each expert's
  * output to bf16 in between).
  *   Of h the configuration (hidden, num_topk, num_experts) and the flag word
  *   are used; its layout is neither needed nor changed, and max_tokens does not
@@ -171,8 +177,9 @@ ep_status ep_moe_workspace_size(const ep_handle* h, const ep_weights* w_up,
  *   d_workspace: 256-byte aligned, at least ep_moe_workspace_size bytes, needs
  *   no clearing; in use by one stream (or graph in flight) at a time.
  *   Two kernels for up to 16 tokens and 64 entries of topk_idx whose activations
- *   fit LDS (64 KB: 4 bytes * entries * I), else three.  The result does not
- *   depend on the order in which blocks run. */
+ *   fit 64 KB of LDS, 2 * entries * (2 * I' + 16) bytes with I' = I rounded up
+ *   to a multiple of 64 (bf16 w_down) or 256 (4 bits); else three.  The result
+ *   does not depend on the order in which blocks run. */
 ep_status ep_moe_layer(const ep_handle* h, const ep_weights* w_up, const ep_weights* w_down,
                        const void* d_x, const int32_t* d_topk_idx, const float* d_topk_weights,
                        int64_t num_tokens, void* d_out, void* d_workspace, int64_t workspace_bytes,
