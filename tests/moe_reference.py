@@ -182,3 +182,50 @@ def gate_grad(logits, idx, g, score, renorm, scale):
         np.add.at(ds, es, gk)
         out[t] = s * (ds - (ds * s).sum()) if score == "softmax" else ds * s * (1 - s)
     return out
+
+
+def gate_grad_bound(logits, idx, g, score, renorm, scale, out_half):
+    """(gate_grad, what an fp32 evaluation and one rounding by out_half may be off
+    it), element by element.  In units u = 2^-24, the relative errors are
+      a score p = exp(a) / sum: |a| for the rounding of a (softmax: a difference
+        of logits; log sigmoid twice that, for its own rounding and the
+        difference's), 4 for the exponential, at most 24 for the sum's additions,
+        4 for the rest: |a| + 32;
+      1 - s: 8;  g * scale: 1;
+    sums of g over K entries lose K + 8 units of the magnitudes they run over."""
+    u = F32_HALF
+    out, err = np.zeros(logits.shape), np.zeros(logits.shape)
+    E, K = logits.shape[1], idx.shape[1]
+    for t in range(idx.shape[0]):
+        ks = [k for k in range(K) if 0 <= idx[t, k] < E]
+        if not ks:
+            continue
+        es = idx[t, ks].astype(int)
+        z, gk = logits[t].astype(np.float64), g[t, ks].astype(np.float64) * scale
+        if score == "softmax":
+            a = z - (z[es] if renorm else z).max()
+            rel = (np.abs(a) + 32) * u
+        else:
+            a = -np.logaddexp(0, -z)
+            rel = (2 * (np.abs(a) + np.abs(a[es]).max()) + 32) * u
+            if renorm:
+                a = a - a[es].max()
+        p = np.exp(a)
+        if renorm:
+            p = p / p[es].sum()
+        elif score == "softmax":
+            p = p / p.sum()
+        dot = (gk * p[es]).sum() if renorm or score == "softmax" else 0.0
+        edot = (np.abs(gk) * p[es] * (rel[es] + (K + 9) * u)).sum() if renorm or score == "softmax" else 0.0
+        if score == "softmax" and not renorm:
+            sg, eg = np.zeros(E), np.zeros(E)
+            np.add.at(sg, es, gk)
+            np.add.at(eg, es, np.abs(gk) * (K + 9) * u)
+            out[t] = p * (sg - dot)
+            err[t] = p * (eg + edot) + np.abs(out[t]) * (rel + 4 * u)
+        else:
+            q = 1 / (1 + np.exp(z[es])) if score == "sigmoid" else np.ones(len(es))
+            d = p[es] * q * (gk - dot)
+            np.add.at(out[t], es, d)
+            np.add.at(err[t], es, p[es] * q * (edot + 2 * u * np.abs(gk)) + np.abs(d) * (rel[es] + (K + 16) * u))
+    return out, err + out_half * (np.abs(out) + err) + 1e-38

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import moe_reference as R
+from test_moe_abi import grad_case
 from combine_get_dispatch_layout_amd import ep, moe
 
 pytestmark = pytest.mark.gpu
@@ -186,3 +187,27 @@ def test_gate_graph_replays():
         idx, w = moe.ep_gate(cfg, lg)
         assert torch.equal(out[0], idx) and torch.equal(out[1], w)
         assert torch.equal(out[2], moe.ep_gate_backward(cfg, lg, idx, gw))
+
+
+# ---- router: gradients, each element to its own bound ------------------------------
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,E,K,shift", [(1, 256, 8, 0), (33, 7, 3, 0), (70, 128, 8, 0), (70, 128, 8, 1), (5, 1024, 16, 0),
+                                         (6, 300, 2, 0), (9, 64, 16, 0), (9, 513, 5, 0), (6, 1, 1, 0), (130, 260, 8, 2)])
+def test_gate_backward_to_each_elements_bound(N, E, K, shift, dtype, renorm, score):
+    """shift: elements by which the output stands off the vectors' alignment."""
+    say(f"[gate grad] {N} {E} {K} {shift} {dtype} {renorm} {score}")
+    z, idx, g = grad_case(N, E, K)
+    lg = torch.from_numpy(z).to(dtype)
+    cfg = moe.GateConfig(E, K, dict(softmax=0, sigmoid=1)[score], renorm, scale=2.5)
+    out = torch.full((N * E + shift + 1,), 77.0, dtype=dtype, device="cuda")
+    got = moe.ep_gate_backward(cfg, lg.cuda(), torch.from_numpy(idx).cuda(), torch.from_numpy(g).cuda(),
+                               out[shift:-1].view(N, E))
+    want, tol = R.gate_grad_bound(lg.float().numpy(), idx, g, score, renorm, 2.5,
+                                  R.BF16_HALF if dtype == torch.bfloat16 else R.F32_HALF)
+    bad = ~(np.abs(got.double().cpu().numpy() - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), got.cpu().numpy()[bad][:4] if dtype ==
+                           torch.float32 else None, want[bad][:4], tol[bad][:4])
+    assert (out[:shift] == 77).all() and out[-1] == 77

@@ -245,3 +245,53 @@ def test_reference_gate_by_hand():
     assert idx.tolist() == [[1, 0]]             # groups {0,1} and {2,3} ... by summed softmax
     idx, _ = R.gate(lg, 2, groups=4, topk_groups=2, group_top=1, limit=True)
     assert idx.tolist() == [[1, 4]]
+
+
+def grad_case(N, E, K, seed=0):
+    """Logits, a choice with masked, foreign and repeated entries, gradients."""
+    rng = np.random.default_rng(seed + N + E)
+    z = (2 * rng.standard_normal((N, E))).astype(np.float32)
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :K].astype(np.int32)
+    idx[rng.random(idx.shape) < 0.1] = -1
+    if N > 4:
+        idx[2] = -1
+        idx[3, 0], idx[3, K - 1] = E, -5
+        idx[4] = idx[4, 0]
+    return z, idx, rng.standard_normal((N, K)).astype(np.float32)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("N,E,K", [(1, 256, 8), (33, 7, 3), (70, 128, 8), (5, 1024, 16), (6, 300, 2)])
+@pytest.mark.parametrize("half", [R.F32_HALF, R.BF16_HALF])
+def test_gradient_bound_sees_what_it_should(half, N, E, K, renorm, score):
+    """The bound holds the definition and tells left-out terms from it."""
+    z, idx, g = grad_case(N, E, K)
+    g = g.astype(np.float64)
+    want, tol = R.gate_grad_bound(z, idx, g, score, renorm, 2.5, half)
+    np.testing.assert_allclose(want, R.gate_grad(z, idx, g, score, renorm, 2.5), rtol=1e-9, atol=1e-12)
+    ok = (idx >= 0) & (idx < E)
+    chosen = np.zeros(z.shape, bool)
+    t, k = ok.nonzero()
+    chosen[t, idx[t, k]] = True
+    live = chosen.any(1)
+    if renorm:      # without the common term
+        p = np.where(ok, R.gate_weights(z.astype(np.float64), idx, score, True, 1.0), 0)
+        q = 1 / (1 + np.exp(z[np.arange(N)[:, None], np.where(ok, idx, 0)])) if score == "sigmoid" else 1.0
+        wrong = np.zeros(z.shape)
+        np.add.at(wrong, (t, idx[t, k]), (2.5 * p * q * g)[t, k])
+        several = (ok.sum(1) > 1)[:, None] & chosen
+        assert (np.abs(wrong - want) > tol)[several].mean() > 0.9
+    if score == "softmax" and not renorm:
+        rest = ~chosen & live[:, None]
+        assert (np.abs(want) > 10 * tol)[rest].mean() > 0.9 if half == R.F32_HALF else \
+            (np.abs(want) > tol)[rest].all()
+        s = np.exp(z - z.max(1, keepdims=True).astype(np.float64))
+        s /= s.sum(1, keepdims=True)
+        gs = np.zeros(z.shape)
+        np.add.at(gs, (t, idx[t, k]), 2.5 * g[t, k])
+        assert (np.abs(s * gs - want) > tol)[live].mean() > 0.9       # no dot term
+    # one bf16 step is outside an fp32 bound
+    if half == R.F32_HALF:
+        big = np.abs(want) > 1e-6
+        assert (np.abs(want * 2.0 ** -9) > tol)[big].mean() > 0.9
