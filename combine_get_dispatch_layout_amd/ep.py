@@ -193,6 +193,10 @@ class Handle:
     """Owns the C handle and keeps its workspace tensor alive (None for the
     library's static handle, whose workspace is the library's own)."""
 
+    # what a layout started by ep_dispatch_overlap reads and writes in
+    # ep_combine_overlap: alive until then, whatever the caller keeps
+    _waiting = None
+
     def __init__(self, cfg: Config, max_tokens: int, workspace: Optional[torch.Tensor], ptr: int,
                  device=None):
         self.cfg = cfg
@@ -337,6 +341,7 @@ def ep_get_layout(h: Handle, topk_idx: torch.Tensor, num_tokens_per_rank=None,
                                _ptr(is_token_in_rank), int(bool(do_cpu_sync)),
                                host_list, ctypes.byref(S) if do_cpu_sync else None,
                                _stream(dev)))
+    h._waiting = None
     out = dict(num_tokens_per_rank=num_tokens_per_rank,
                num_tokens_per_rdma_rank=num_tokens_per_rdma_rank,
                num_tokens_per_expert=num_tokens_per_expert, is_token_in_rank=is_token_in_rank)
@@ -373,6 +378,7 @@ def ep_layout_dispatch(h: Handle, topk_idx: torch.Tensor, x: torch.Tensor, recv_
     _check(lib().ep_layout_dispatch(h.ptr, _ptr(topk_idx), topk_idx.shape[0], *map(_ptr, outs),
                                     _ptr(x), _ptr(recv_x), _ptr(recv_scales), recv_x.shape[0],
                                     _stream(x.device)))
+    h._waiting = None
     return dict(num_tokens_per_rank=outs[0], num_tokens_per_rdma_rank=outs[1],
                 num_tokens_per_expert=outs[2], is_token_in_rank=outs[3])
 
@@ -450,6 +456,7 @@ def ep_dispatch_overlap(h: Handle, x: torch.Tensor, recv_x: torch.Tensor,
                                      n_next, *map(_ptr, outs), _stream(x.device)))
     if h_next is None:
         return None
+    h_next._waiting = (topk_next, *outs)
     return dict(num_tokens_per_rank=outs[0], num_tokens_per_rdma_rank=outs[1],
                 num_tokens_per_expert=outs[2], is_token_in_rank=outs[3])
 
@@ -463,6 +470,8 @@ def ep_combine_overlap(h: Handle, y: torch.Tensor, topk_weights: Optional[torch.
     _check(lib().ep_combine_overlap(h.ptr, _ptr(y), _ptr(y_scales), y.shape[0], _ptr(topk_weights),
                                     token_begin, token_end, _ptr(out),
                                     h_next.ptr if h_next is not None else None, _stream(out.device)))
+    if h_next is not None:
+        h_next._waiting = None
     return out
 
 

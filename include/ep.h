@@ -336,8 +336,8 @@ ep_status ep_combine(const ep_handle* h, const void* d_y, const float* d_y_scale
  *   under 4 MiB (one source, expand form) the layout completes in this
  *   launch; otherwise it completes in the next ep_combine_overlap(...,
  *   h_next) call,
- *   and until then h_next may be used only there (other calls return
- *   EP_ERR_STATE; ep_get_layout, ep_layout_dispatch or another
+ *   and until then d_topk_next and the four outputs stay valid and h_next may
+ *   be used only there (other calls return EP_ERR_STATE; ep_get_layout, ep_layout_dispatch or another
  *   ep_dispatch_overlap naming it as h_next start over, discarding the
  *   counted part).
  *   Configurations whose layout cannot share the launches (num_topk > 8,
