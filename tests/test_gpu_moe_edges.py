@@ -211,3 +211,26 @@ def test_gate_backward_to_each_elements_bound(N, E, K, shift, dtype, renorm, sco
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), got.cpu().numpy()[bad][:4] if dtype ==
                            torch.float32 else None, want[bad][:4], tol[bad][:4])
     assert (out[:shift] == 77).all() and out[-1] == 77
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [0, 8])
+def test_gate_infinite_and_huge_biases(groups, score):
+    """Biases of +infinity (chosen first, by id), near the largest float (sums of
+    a group past fp32) and of both signs: the choice's order is the definition's,
+    the weights know none of it."""
+    rng = np.random.default_rng(7)
+    E, K = 64, 6
+    lg = rng.standard_normal((30, E)).astype(np.float32)
+    kw = dict(num_groups=groups, topk_groups=3, group_top=2) if groups else {}
+    rkw = dict(groups=groups, topk_groups=3, group_top=2) if groups else {}
+    for special in ({5: np.inf}, {3: np.inf, 4: np.inf, 40: np.inf, 41: np.inf}, {8: 3.4e38, 9: 3.4e38, 50: 3.4e38},
+                    {i: -3.4e38 for i in range(E)}, {20: np.inf, 21: -np.inf, 22: -3.4e38, 23: np.nan}):
+        bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+        for e, v in special.items():
+            bias[e] = v
+        cfg = moe.GateConfig(E, K, dict(softmax=0, sigmoid=1)[score], **kw)
+        idx, w = moe.ep_gate(cfg, torch.from_numpy(lg).cuda(), torch.from_numpy(bias).cuda())
+        ridx, rw = R.gate(lg, K, score, bias=bias, **rkw)
+        assert np.array_equal(idx.cpu().numpy(), ridx), special
+        assert np.allclose(w.cpu().numpy(), rw, rtol=2 * R.F32_HALF, atol=1e-44)

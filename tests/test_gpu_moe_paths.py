@@ -339,3 +339,106 @@ def test_layer_handful_limits(fmt, group, N, K, I, two):
     assert (paths[1] == 0) == two
     c = run_layer(paths, N, 17, K, 256, I, fmt, group, fmt == "int4" and group != 64, 0.05)
     check_isolation(*c)
+
+
+# ---- calls side by side ------------------------------------------------------------------
+
+MIXED = [(("bf16", 0, False), ("mxfp4", 32, False)), (("mxfp4", 32, False), ("int4", 128, False)),
+         (("int4", 32, True), ("bf16", 0, False)), (("int4", 64, False), ("int4", 32, True))]
+
+
+@pytest.mark.parametrize("kinds", MIXED)
+@pytest.mark.parametrize("N,E,K,H,I", [(1, 8, 2, 256, 128), (7, 8, 2, 384, 256), (40, 8, 3, 256, 384), (48, 64, 4, 1152, 640)])
+def test_layer_of_two_formats(N, E, K, H, I, kinds):
+    say(f"[two formats] {N} {H} {I} {kinds}")
+    up, down = Stack(*kinds[0], E, 2 * I, H, 1), Stack(*kinds[1], E, H, I, 2)
+    idx, wts = routed(N, E, K, 0.1, seed=N)
+    x = randn(N, H, 3)
+    h = ep.ep_handle_init(ep.Config(hidden=H, num_topk=K, num_experts=E, num_ranks=1), 1)
+    close(moe.ep_moe_layer(h, up.w, down.w, x, idx, wts), *layer64(x, idx, wts, up, down))
+
+
+def test_calls_at_once_on_two_streams():
+    """Layers and products in flight together, sharing weights and the handle."""
+    E, K, H, I, N = 64, 4, 1152, 640, 48
+    up, down = Stack("mxfp4", 32, False, E, 2 * I, H, 1), Stack("mxfp4", 32, False, E, H, I, 2)
+    h = ep.ep_handle_init(ep.Config(hidden=H, num_topk=K, num_experts=E, num_ranks=1), N)
+    idx, wts = routed(N, E, K, 0.1, seed=1)
+    ep.ep_get_layout(h, idx)
+    recv = randn(N * K, H, 5)
+    xs = [randn(N, H, 6 + i) for i in range(2)]
+    want = [moe.ep_moe_layer(h, up.w, down.w, x, idx, wts) for x in xs]
+    y0 = moe.ep_expert_matvec(h, up.w, recv, torch.zeros((N * K, I), dtype=torch.bfloat16, device="cuda"), activation=1)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(moe.ep_moe_layer(h, up.w, down.w, xs[i], idx, wts))
+                got[i].append(moe.ep_expert_matvec(h, up.w, recv, torch.zeros_like(y0), activation=1))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in range(5):
+            assert torch.equal(got[i][2 * r], want[i]) and torch.equal(got[i][2 * r + 1], y0)
+    assert ep.ep_check_error(h) == (ep.EP_OK, 0)
+
+
+@pytest.mark.parametrize("E,K,H,I,N", [(16, 3, 256, 128, 30), (64, 4, 1024, 640, 48)])
+def test_shuffled_path_graph_replays(E, K, H, I, N):
+    """Router, layout, dispatch, both products and combine as one graph, against
+    the eager calls, with new logits and eager work between the replays."""
+    up, down = Stack("int4", 64, True, E, 2 * I, H, 1), Stack("int4", 64, True, E, H, I, 2)
+    cfg = ep.Config(hidden=H, num_topk=K, num_experts=E, num_ranks=1, expert_alignment=2)
+    gcfg = moe.GateConfig(E, K, moe.EP_SCORE_SIGMOID)
+    rows = ep.ep_recv_capacity(cfg, N)
+    lg, x = torch.randn((N, E), device="cuda"), randn(N, H, 1)
+    new = lambda r, c: torch.zeros((r, c), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+
+    def make():
+        return dict(h=ep.ep_handle_init(cfg, N), recv=new(rows, H), act=new(rows, I), y=new(rows, H), out=new(N, H),
+                    idx=torch.zeros((N, K), dtype=torch.int32, device="cuda"), w=torch.zeros((N, K), device="cuda"))
+
+    def step(b):
+        moe.ep_gate(gcfg, lg, topk_idx=b["idx"], topk_weights=b["w"])
+        ep.ep_get_layout(b["h"], b["idx"], alloc_outputs=False)
+        ep.ep_dispatch(b["h"], x, b["recv"])
+        moe.ep_expert_matvec(b["h"], up.w, b["recv"], b["act"], activation=1)
+        moe.ep_expert_matvec(b["h"], down.w, b["act"], b["y"])
+        ep.ep_combine(b["h"], b["y"], b["w"], b["out"])
+
+    a, b = make(), make()
+    step(a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(a)
+    for i in range(4):
+        lg.normal_()
+        x.copy_(randn(N, H, 20 + i))
+        a["out"].fill_(77)
+        graph.replay()
+        step(b)
+        torch.cuda.synchronize()
+        assert torch.equal(a["idx"], b["idx"]) and torch.equal(a["out"], b["out"]), i
+    for c in (a, b):
+        assert ep.ep_check_error(c["h"]) == (ep.EP_OK, 0)
+
+
+def test_layout_that_waits_is_refused():
+    """A layout that the next combine finishes is not there yet."""
+    cfg = ep.Config(hidden=64, num_topk=2, num_experts=8, num_ranks=1)
+    h, nxt = ep.ep_handle_init(cfg, 4000), ep.ep_handle_init(cfg, 4000)
+    idx, wts = routed(4000, 8, 2, seed=1)
+    ep.ep_get_layout(h, idx)
+    recv, x, out = randn(8000, 64, 1), randn(4000, 64, 2), randn(4000, 64, 3)
+    ep.ep_dispatch_overlap(h, x, recv, h_next=nxt, topk_next=idx)
+    st = Stack("bf16", 0, False, 8, 40, 64, 1)
+    want = moe.ep_expert_matvec(h, st.w, recv)
+    try:
+        got = moe.ep_expert_matvec(nxt, st.w, recv)
+    except ep.EpError as e:
+        assert e.status == ep.EP_ERR_STATE
+        ep.ep_combine_overlap(h, recv, wts, out, h_next=nxt)
+        got = moe.ep_expert_matvec(nxt, st.w, recv)
+    assert torch.equal(got, want)
