@@ -927,7 +927,7 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
 
 // ---- the down projection of a handful of tokens, with the sum over their experts ---
 //
-// Up to 16 tokens and 64 pairs whose activations fit LDS.  A block owns 16
+// Up to 16 tokens and 32 (or 8) pairs whose activations fit LDS.  A block owns 16
 // outputs of every token.  Row m of the A operand is token m's activation for
 // the expert whose weights are in B, so a token's experts add up in the same
 // accumulators and nothing has to be combined afterwards.  Tokens that the
@@ -1104,7 +1104,7 @@ __global__ __launch_bounds__(kFewWaves* kWave, 4) void k_down_few(ProductArgs a)
 template <int KIND>
 hipError_t launch_down_few(const ProductArgs& a, bool* done, hipStream_t s)
 {
-    static_assert(kFewPairs == kWave, "a pair a lane");
+    static_assert(few_pairs(KIND) <= kWave, "a pair a lane");
     *done = few_fits(KIND, a.P / a.K, a.P, a.w.cols);
     if (!*done) return hipSuccess;
     const int64_t lds = few_bytes(KIND, a.P, a.w.cols);

@@ -46,6 +46,18 @@ constexpr int two_tile_waves(int kind) { return kind >= kInt4G32 ? 4 : 8; }
 // Waves of the big blocks (one of eight waves a CU) that run at a time.
 constexpr int64_t kAtOnce = 2048;
 
+// Few tiles: blocks of four waves and short rings, two or three to a CU.
+// Small blocks' time over big ones', 2048 columns (MXFP4, bf16, INT4):
+//   128 tiles  0.78 1.06 0.93   8 us
+//   256        0.84 1.03 0.96
+//   384        0.97 0.97 1.00
+//   512        1.03 1.03 1.07   11, 18, 14 us with big blocks
+//   640        1.25 1.19 1.15
+//   768        1.31 1.19 1.19
+//   1984       1.68 1.13 1.45   17, 41, 23 us
+//   8192       1.62 1.41 1.67
+constexpr int64_t kSmallTiles = 512;
+
 enum Path {
     kPathNone = 0,      // no rows
     kPathSmall = 1,     // blocks of four waves
@@ -84,12 +96,7 @@ inline Shape choose_shape(int kind, bool gate, int planes, int64_t cols, int64_t
         while (kw < most && kw * 2 <= blocks && s.tiles * kw * 2 <= at_once) kw *= 2;
         return kw;
     };
-    // Few tiles (less than one a wave of the big blocks): blocks of four waves
-    // and short rings, two or three to a CU.  At one and the same step of the
-    // kernel one token through the bf16 layer took 28.4 us so and 30.4 us with
-    // the big blocks alone; a decode batch (32768 tiles) 1374 us so and 816 us
-    // with them.
-    if (tt == 1 && s.tiles < kAtOnce) {
+    if (tt == 1 && s.tiles < kSmallTiles) {
         s.kw = waves_per_tile(4, kSpansSmall, 4 * kAtOnce);
         const int64_t fit = (kLdsSmall - sums_bytes(4, s.kw, 1)) / stride;
         if (fit >= likely) {
@@ -119,8 +126,18 @@ inline Shape choose_shape(int kind, bool gate, int planes, int64_t cols, int64_t
 // ---- a layer's down projection of a handful of tokens ------------------------
 
 constexpr int kFewWaves = 16;
-constexpr int kFewTokens = 16;
-constexpr int kFewPairs = 64;
+constexpr int kFewTokens = 16;      // rows of the operand
+
+// Pairs up to which it is no slower than the general kernel and the sum behind
+// it.  Its time of a layer over theirs (2048 x 768, 512 or 256):
+//   pairs            4     8        16 and 20   32          48
+//   MXFP4            0.77  0.83     0.85-0.97   0.91-0.98   1.01
+//   bf16             0.89  0.91     0.81-0.91   0.99-1.05   1.04-1.07
+//   INT4, 128        0.74  0.86     0.88-1.03   0.97-1.03   1.02-1.04
+//   INT4, 64         0.83  1.02     1.03-1.24   1.03-1.10   1.09
+//   INT4, 32         0.84  0.98     1.00-1.17   1.07-1.12   1.13-1.15
+// (the scales of small groups are loaded one by one here).
+constexpr int few_pairs(int kind) { return kind == kInt4G32 || kind == kInt4G64 ? 8 : 32; }
 
 // Its LDS: the pairs' activations in two terms, or the waves' sums.
 constexpr int64_t few_bytes(int kind, int64_t pairs, int64_t cols)
@@ -131,7 +148,7 @@ constexpr int64_t few_bytes(int kind, int64_t pairs, int64_t cols)
 
 constexpr bool few_fits(int kind, int64_t tokens, int64_t pairs, int64_t cols)
 {
-    return pairs <= kFewPairs && tokens <= kFewTokens && few_bytes(kind, pairs, cols) <= kLdsSmall;
+    return pairs <= few_pairs(kind) && tokens <= kFewTokens && few_bytes(kind, pairs, cols) <= kLdsSmall;
 }
 
 }  // namespace prod

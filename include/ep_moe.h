@@ -176,10 +176,11 @@ ep_status ep_moe_workspace_size(const ep_handle* h, const ep_weights* w_up,
  *   expert gets +0.  d_out may be d_x.
  *   d_workspace: 256-byte aligned, at least ep_moe_workspace_size bytes, needs
  *   no clearing; in use by one stream (or graph in flight) at a time.
- *   Two kernels for up to 16 tokens and 64 entries of topk_idx whose activations
- *   fit 64 KB of LDS, 2 * entries * (2 * I' + 16) bytes with I' = I rounded up
- *   to a multiple of 64 (bf16 w_down) or 256 (4 bits); else three.  The result
- *   does not depend on the order in which blocks run. */
+ *   Two kernels for up to 16 tokens and 32 entries of topk_idx (8 with w_down in
+ *   INT4 groups of 32 or 64) whose activations fit 64 KB of LDS, 2 * entries *
+ *   (2 * I' + 16) bytes with I' = I rounded up to a multiple of 64 (bf16 w_down)
+ *   or 256 (4 bits); else three.  The result does not depend on the order in
+ *   which blocks run. */
 ep_status ep_moe_layer(const ep_handle* h, const ep_weights* w_up, const ep_weights* w_down,
                        const void* d_x, const int32_t* d_topk_idx, const float* d_topk_weights,
                        int64_t num_tokens, void* d_out, void* d_workspace, int64_t workspace_bytes,

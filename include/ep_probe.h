@@ -62,7 +62,7 @@ int ep_probe_rows(int mode, const void* d_src, void* d_dst, const int32_t* d_slo
  * num_topk of the layout or layer. */
 enum {
     EP_PATH_NONE = 0,       /* no rows                                         */
-    EP_PATH_SMALL = 1,      /* fewer tiles than waves: blocks of four waves    */
+    EP_PATH_SMALL = 1,      /* few tiles: blocks of four waves                 */
     EP_PATH_ONE_TILE = 2,   /* up to 16 rows at once, x in LDS                 */
     EP_PATH_MEMORY = 3,     /* the same, x does not fit LDS                    */
     EP_PATH_TWO_TILES = 4   /* up to 32 rows at once                           */

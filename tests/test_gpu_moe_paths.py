@@ -147,13 +147,15 @@ def run_experts(path, idx, E, M, C, fmt, group, zeros, align=1, acts=(0, 1), see
                 close(y[s], want, err, (fmt, act, e))
 
 
-# ---- 16 rows at once, x in LDS: 2048 tiles and more ---------------------------------
+# ---- 16 rows at once, x in LDS: 512 tiles and more ----------------------------------
 
 @pytest.mark.parametrize("fmt,group,zeros", KINDS)
 @pytest.mark.parametrize("N,E,K,M,C,mask,skew,align", [
     (48, 64, 4, 2060, 384, 0.1, 1.5, 1),    # a partial last line; scale rows of 3, 6 and 12
     (48, 64, 4, 2060, 1024, 0.0, 1.5, 4),   # whole lines
     (60, 33, 8, 2062, 1664, 0.0, 0.0, 1),   # scale rows of 13, 26 and 52
+    (20, 16, 3, 1050, 2176, 0.0, 0.0, 1),   # two or four waves share a tile's columns
+    (20, 18, 3, 2062, 2048, 0.0, 0.0, 1),
 ])
 def test_experts_one_tile(N, E, K, M, C, mask, skew, align, fmt, group, zeros):
     """Blocks take several steps of eight tiles and end inside an expert."""
@@ -284,12 +286,15 @@ def nan_expert(st, e):
 
 def check_isolation(h, up, down, x, idx, wts, want):
     """One expert's weights become NaN: only the tokens that chose it see it."""
-    e = int(idx[0, 0])
+    live = [e for e in idx.unique().tolist() if e >= 0 and not (idx == e).any(1).all()]
+    if not live:
+        assert idx.shape[0] == 1
+        return
+    e = live[0]
     nan_expert(up, e)
     nan_expert(down, e)
     got = moe.ep_moe_layer(h, up.w, down.w, x, idx, wts)
     hit = (idx == e).any(1)
-    assert hit.any() and not hit.all()
     assert torch.equal(got[~hit], want[~hit]) and not torch.isfinite(got[hit]).any()
 
 
@@ -327,12 +332,13 @@ def test_layer_two_tiles(fmt, group, zeros):
 # the largest batches whose experts are added inside the down projection, and
 # one step above each
 @pytest.mark.parametrize("fmt,group,N,K,I,two", [
-    ("bf16", 0, 16, 4, 192, True), ("bf16", 0, 16, 4, 200, False), ("bf16", 0, 13, 5, 64, False),
-    ("bf16", 0, 17, 2, 64, False), ("mxfp4", 32, 16, 3, 256, True), ("mxfp4", 32, 15, 4, 256, True),
-    ("mxfp4", 32, 9, 7, 256, False), ("mxfp4", 32, 16, 4, 32, False), ("mxfp4", 32, 10, 3, 512, True),
-    ("mxfp4", 32, 8, 4, 512, False), ("int4", 32, 16, 3, 256, True), ("int4", 32, 15, 4, 224, True),
-    ("int4", 64, 15, 4, 256, True), ("int4", 64, 16, 4, 64, False), ("int4", 128, 12, 5, 256, True),
-    ("int4", 128, 9, 7, 128, False), ("int4", 128, 4, 15, 256, True), ("int4", 64, 16, 1, 768, True), ("int4", 64, 16, 1, 832, False)])
+    ("bf16", 0, 16, 2, 448, True), ("bf16", 0, 16, 2, 456, False), ("bf16", 0, 11, 3, 64, False),
+    ("bf16", 0, 17, 1, 64, False), ("bf16", 0, 2, 16, 448, True), ("mxfp4", 32, 16, 2, 256, True),
+    ("mxfp4", 32, 15, 2, 512, True), ("mxfp4", 32, 16, 2, 512, False), ("mxfp4", 32, 11, 3, 256, False),
+    ("mxfp4", 32, 16, 1, 768, True), ("mxfp4", 32, 16, 1, 1024, False), ("int4", 128, 8, 4, 256, True),
+    ("int4", 128, 15, 2, 384, True), ("int4", 128, 3, 11, 256, False), ("int4", 64, 1, 8, 1728, True),
+    ("int4", 64, 8, 1, 832, True), ("int4", 64, 9, 1, 832, False), ("int4", 32, 2, 4, 1760, True),
+    ("int4", 32, 4, 2, 224, True), ("int4", 32, 3, 3, 224, False)])
 def test_layer_handful_limits(fmt, group, N, K, I, two):
     say(f"[handful] {N} {K} {I} {fmt} {group}")
     paths = P.layer(fmt, group, N, K, 17, 256, I)

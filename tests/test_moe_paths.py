@@ -25,10 +25,10 @@ def test_paths_of_ordinary_sizes(fmt, group):
 
 @pytest.mark.parametrize("fmt,group", KINDS)
 def test_tiles_decide_between_small_and_big_blocks(fmt, group):
-    """2048 tiles of 32 outputs (16 with a gate)."""
+    """512 tiles of 32 outputs (16 with a gate)."""
     for act in (0, 1):
-        assert P.product(fmt, group, 256, 32 * 31, 64, 64, act)[0] == P.SMALL
-        assert P.product(fmt, group, 256, 32 * 31 + 2, 64, 64, act)[0] == P.ONE_TILE
+        assert P.product(fmt, group, 256, 32 * 31, 16, 16, act)[0] == P.SMALL
+        assert P.product(fmt, group, 256, 32 * 31 + 2, 16, 16, act)[0] == P.ONE_TILE
     # or rows that the small blocks' LDS does not hold
     assert P.product(fmt, group, 32768, 32, 1, 1)[0] == P.ONE_TILE
     assert P.product(fmt, group, 65536, 32, 1, 1)[0] == P.MEMORY
@@ -46,10 +46,11 @@ def test_rows_at_once_never_fall_below_the_mean(fmt, group):
 
 def test_limits_of_a_handful():
     """64 KB hold the pairs' two terms in rows of whole lines and 16 bytes."""
-    for fmt, group, line in (("bf16", 0, 64), ("mxfp4", 32, 256), ("int4", 128, 256)):
+    for fmt, group, line, most in (("bf16", 0, 64, 32), ("mxfp4", 32, 256, 32), ("int4", 128, 256, 32),
+                                   ("int4", 64, 256, 8), ("int4", 32, 256, 8)):
         for I in (128, 256, 512, 1024, 2048):
             for N in range(1, 18):
                 for K in range(1, 17):
                     row = 2 * (-(-I // line) * line) + 16
-                    fits = N <= 16 and N * K <= 64 and 2 * N * K * row <= 65536
+                    fits = N <= 16 and N * K <= most and 2 * N * K * row <= 65536
                     assert (P.layer(fmt, group, N, K, 64, 256, I)[1] == 0) == fits
