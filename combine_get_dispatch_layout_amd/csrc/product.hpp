@@ -11,8 +11,15 @@
 // What bounds it: the weights are read from HBM once and used for few rows, so
 // everything serves keeping 16-byte weight loads in flight.  They go straight
 // from memory to registers (no LDS round trip, nothing to share between
-// waves), a block of 4 spans per tile ahead of the arithmetic; only x, which
-// every wave of a block reads, goes through LDS.
+// waves), a block of spans per tile ahead of the arithmetic: four, or two in
+// the small blocks, with INT4 groups of 32 and with 4-bit weights beside x from
+// memory.  Only x, which every wave of a block reads, goes through LDS.
+//
+// Scales come a block ahead too, as whole words, where a row has a multiple of
+// four of them.  Other rows (and a row's last, partial block) load them span by
+// span behind the ring's own loads, whose order they then wait for: 64 experts,
+// 4096 outputs, 2816 columns of MXFP4 86 us, 2880 columns 141 us; INT4 in groups
+// of 128, 1024 columns 44 us, 768 columns 59 us.
 //
 // A lane's 16 bytes and the order of the columns.  A sum over columns may run
 // in any order as long as x and W agree.  A load takes 8 rows x 128 bytes
@@ -33,15 +40,16 @@
 //          away in fp32; the group's scale multiplies the fp32 sum, so no
 //          weight is rounded.  16 is the smallest offset that leaves all codes
 //          one exponent: what the fp32 sums lose and the x at which they
-//          overflow go with it.  (Without the second instruction the 128-token
-//          layer would take 1153 us instead of 1314: the price of exact codes.)
+//          overflow go with it.  (The second instruction is an eighth of the
+//          128-token layer's time: the price of exact codes.)
 //
 // Measured on MI355X (GPU time): the up projection of a decode batch (128
 // tokens, 256 experts, top-8, 7168 columns, 2 x 2048 rows, MXFP4, 4.0 GB)
-// 667 us, 5.9 TB/s; in INT4 816 us, 4.7 TB/s, where the arithmetic of two
-// waves a SIMD no longer hides behind the loads; without any arithmetic 1060 us
-// of the whole INT4 layer's 1314.  Twelve or sixteen waves a CU with shorter
-// rings are slower (790 and more): fewer bytes in flight.
+// 667 us, 5.9 TB/s; in bf16 2176 us, 6.8 TB/s; in INT4 (groups of 128) 809 us,
+// 4.7 TB/s, where the arithmetic of two waves a SIMD no longer hides behind the
+// loads: without any, the whole INT4 layer takes 1060 us of its 1350.  Twelve or
+// sixteen waves a CU with shorter rings are slower (790 us and more for MXFP4):
+// fewer bytes in flight.
 #pragma once
 
 #include "experts.hpp"
@@ -290,9 +298,12 @@ __device__ __forceinline__ u32x4 pair_columns(u32x4 d)
                  __builtin_amdgcn_perm(d[3], d[1], 0x07060302u)};
 }
 
+// __expf's argument is off by 2^-24 of itself, so silu by |gate| * 2^-24 of it:
+// far below the 2^-17 that the two terms below hold for any |gate| whose silu
+// does not vanish (< 88), and the 2^-9 of a bf16 result.
 __device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.f + __expf(-gate)) * up; }
 
-// y + y_lo = w * swiglu: two bf16 terms hold 16 bits of the fp32 value (an
+// y + y_lo = w * swiglu: two bf16 terms hold at least 16 bits of the fp32 value (an
 // infinity or NaN stays in the first), so the down projection, which takes
 // bf16 operands, loses 2^-17 of it and not 2^-9.
 __device__ __forceinline__ void store_split(const ProductArgs& a, int64_t row, int u, float gate, float up)
@@ -447,7 +458,10 @@ constexpr int kListRows = 128;      // ... and their rows, at most
 // tile of the batch, and its kw waves every kw-th block of kU spans of the
 // tile's columns.  RT = 2: 16-output tiles of a wave (with a gate: its gate
 // tile and its up tile); TT: 16-row tiles of x.
-// DIRECT: x is read from memory, a block ahead, not through LDS.
+// DIRECT: x is read from memory, a block ahead, not through LDS.  With 4-bit
+// weights and two terms of x (a layer's down projection) the compiler keeps that
+// block in private memory (272 bytes a lane), so the loads ahead gain little
+// there: 64 tokens, 8 experts, 4096 x 14336, INT4: 977 us for a floor of 100.
 template <int KIND, int EPI, int TT, bool DIRECT, int kU, int kWaves>
 __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kWaves == 4 ? (KIND <= kMxfp4 ? 3 : 2) : kWaves / 4) void k_product(ProductArgs a)
 {
