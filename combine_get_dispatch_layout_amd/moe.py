@@ -129,10 +129,16 @@ class _Gate(torch.autograd.Function):
     """ep_gate with ep_gate_backward as its weights' gradient."""
 
     @staticmethod
-    def forward(ctx, cfg, logits, bias, token_mask):
-        topk_idx, topk_weights = ep_gate(cfg, logits, bias, token_mask)
-        ctx.cfg = cfg
-        ctx.save_for_backward(logits, topk_idx)
+    def forward(ctx, cfg, logits, bias, token_mask, given_idx, given_weights):
+        topk_idx, topk_weights = ep_gate(cfg, logits, bias, token_mask, given_idx, given_weights)
+        ctx.cfg, ctx.leaf = cfg, logits.is_leaf
+        # a given buffer may be filled again before the backward pass
+        ctx.save_for_backward(logits, topk_idx if given_idx is None else topk_idx.clone())
+        # outputs of their own, in the given memory: the buffers keep no graph
+        if given_idx is not None:
+            topk_idx = topk_idx.detach()
+        if given_weights is not None:
+            topk_weights = topk_weights.detach()
         ctx.mark_non_differentiable(topk_idx)
         ctx.set_materialize_grads(False)
         return topk_idx, topk_weights
@@ -140,11 +146,17 @@ class _Gate(torch.autograd.Function):
     @staticmethod
     def backward(ctx, _, grad_weights):
         if grad_weights is None:
-            return None, None, None, None
+            return (None,) * 6
         if torch.is_grad_enabled():     # create_graph: would lose the second order silently
             raise RuntimeError("ep_gate has a first order gradient only")
+        # a leaf's gradient accumulates on the stream of its first use, which a
+        # captured backward pass must not touch
+        if ctx.leaf and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the backward pass of ep_gate into leaf logits must not be captured: "
+                               "capture ep_gate_backward")
         logits, topk_idx = ctx.saved_tensors
-        return None, ep_gate_backward(ctx.cfg, logits, topk_idx, grad_weights.contiguous()), None, None
+        grad = ep_gate_backward(ctx.cfg, logits, topk_idx, grad_weights.contiguous())
+        return None, grad, None, None, None, None
 
 
 def ep_gate(cfg: GateConfig, logits: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -153,18 +165,11 @@ def ep_gate(cfg: GateConfig, logits: torch.Tensor, bias: Optional[torch.Tensor] 
     """Chooses num_topk experts per row of logits [N, E] (fp32 or bf16).  bias
     fp32 [E] acts on the choice only; token_mask bool / uint8 [N]: rows with 0
     get none.  Returns (topk_idx int32 [N,K], topk_weights fp32 [N,K]).  Where
-    autograd records and the logits require a gradient, the weights have one
-    (the choice held fixed); both outputs are then allocated here, and leaf
-    logits are refused inside a graph capture."""
+    autograd records and the logits require a gradient, the returned weights
+    have one, the choice held fixed (a topk_weights passed in is filled, but it
+    is the returned tensor that has the gradient)."""
     if logits.requires_grad and torch.is_grad_enabled():
-        if topk_idx is not None or topk_weights is not None:
-            raise ValueError("topk_idx and topk_weights must be left out where the logits require a gradient")
-        # a leaf's gradient accumulates on the stream of its first use, which a
-        # backward pass in the capture must not touch
-        if logits.is_leaf and logits.is_cuda and torch.cuda.is_current_stream_capturing():
-            raise ValueError("leaf logits that require a gradient must not be used in a graph capture: "
-                             "capture ep_gate (without autograd) and ep_gate_backward")
-        return _Gate.apply(cfg, logits, bias, token_mask)
+        return _Gate.apply(cfg, logits, bias, token_mask, topk_idx, topk_weights)
     N, dev = _check_logits(cfg, logits)
     shape = (N, cfg.num_topk)
     if topk_idx is None:

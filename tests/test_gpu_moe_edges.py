@@ -139,13 +139,36 @@ def test_gate_weights_have_the_gradient(score, renorm, dtype):
         assert torch.equal(r.grad, x.t() @ moe.ep_gate_backward(cfg, z.detach(), i, gw))
 
 
-def test_gate_gradient_refuses_given_outputs_and_second_order():
+def test_gate_gradient_with_given_outputs():
+    """Buffers that every step fills again: they keep no graph, and each step's
+    gradient is that of its own choice."""
+    cfg = moe.GateConfig(8, 2)
+    a, b = (torch.randn((5, 8), device="cuda", requires_grad=True) for _ in range(2))
+    idx, w = torch.empty((5, 2), dtype=torch.int32, device="cuda"), torch.empty((5, 2), device="cuda")
+    gw = torch.randn((5, 2), device="cuda")
+    want = []
+    for z in (a, b):
+        with torch.no_grad():
+            i, _ = moe.ep_gate(cfg, z)
+            want.append(moe.ep_gate_backward(cfg, z, i, gw))
+    ia, wa = moe.ep_gate(cfg, a, topk_idx=idx, topk_weights=w)
+    assert ia.data_ptr() == idx.data_ptr() and wa.data_ptr() == w.data_ptr()
+    assert wa.requires_grad and not w.requires_grad and w.grad_fn is None
+    _, wb = moe.ep_gate(cfg, b, topk_idx=idx, topk_weights=w)
+    with torch.no_grad():
+        assert torch.equal(w, moe.ep_gate(cfg, b)[1])
+    wa.backward(gw)
+    wb.backward(gw)
+    assert torch.equal(a.grad, want[0]) and torch.equal(b.grad, want[1])
+    for kw in (dict(topk_idx=idx), dict(topk_weights=w)):
+        a.grad = None
+        moe.ep_gate(cfg, a, **kw)[1].backward(gw)
+        assert torch.equal(a.grad, want[0])
+
+
+def test_gate_gradient_refusals():
     cfg = moe.GateConfig(8, 2)
     lg = torch.randn((3, 8), device="cuda", requires_grad=True)
-    with pytest.raises(ValueError, match="left out"):
-        moe.ep_gate(cfg, lg, topk_idx=torch.empty((3, 2), dtype=torch.int32, device="cuda"))
-    with pytest.raises(ValueError, match="left out"):
-        moe.ep_gate(cfg, lg, topk_weights=torch.empty((3, 2), device="cuda"))
     _, w = moe.ep_gate(cfg, lg)
     with pytest.raises(RuntimeError, match="first order"):
         torch.autograd.grad(w[:, 0].sum(), lg, create_graph=True)
@@ -155,8 +178,12 @@ def test_gate_gradient_refuses_given_outputs_and_second_order():
         w.sum().backward()
     with pytest.MonkeyPatch.context() as mp:        # as inside a capture
         mp.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
-        with pytest.raises(ValueError, match="capture"):
-            moe.ep_gate(cfg, lg)
+        _, w = moe.ep_gate(cfg, lg)
+        with pytest.raises(RuntimeError, match="captured"):
+            w.sum().backward()
+        z = lg * 2                                  # not a leaf
+        moe.ep_gate(cfg, z)[1][:, 0].sum().backward()
+    assert lg.grad is not None
     empty = torch.zeros((0, 8), device="cuda", requires_grad=True)
     moe.ep_gate(cfg, empty)[1].sum().backward()
     assert empty.grad.shape == (0, 8)
