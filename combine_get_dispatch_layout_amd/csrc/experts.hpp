@@ -12,10 +12,10 @@ constexpr int kMaxPairs = 4096;
 
 struct WeightArgs {
     const uint8_t* data;
-    const uint8_t* scales;
+    const uint8_t* scales;      // kInt8: fp32, one a row
     const uint8_t* zeros;       // nullptr: 8 everywhere
     int kind;
-    int rows, cols;             // M, C
+    int rows, cols;             // M, C (kInt8: C / 2)
     int64_t row_bytes;          // of data
     int64_t row_groups;         // scales per row
 };
@@ -44,7 +44,8 @@ struct ProductArgs {
     int P, K;                   // pairs, and pairs per token
     bool x_per_pair;            // pairs: x row = p (else the token p / K)
     const float* weights;       // pairs: [P] or null
-    const uint16_t* x;          // bf16 [.., ldx]
+    const uint16_t* x;          // bf16 [.., ldx]; kInt8: int8 [.., 2 ldx]
+    const float* x_scales;      // kInt8: of each row of x
     const uint16_t* x_lo;       // its second term (kStoreF32), or null
     int64_t ldx;
     void* y;

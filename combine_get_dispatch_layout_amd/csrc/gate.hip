@@ -10,7 +10,7 @@
 // A choice is a whole number, so it has to be right where two experts all but
 // tie: order is decided in fp64, or by the logits themselves where no bias
 // enters (s is strictly increasing in l).
-#include "experts.hpp"
+#include "router.hpp"
 
 namespace epk {
 namespace {
@@ -27,56 +27,6 @@ constexpr int64_t kGridRow = 1 << 20;
 __device__ __forceinline__ int64_t first_token()
 {
     return ((int64_t)blockIdx.y * kGridRow + blockIdx.x) * kGateWaves;
-}
-
-__device__ __forceinline__ float load_logit(const void* p, bool bf16, int64_t i)
-{
-    if (bf16) return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << 16);
-    return reinterpret_cast<const float*>(p)[i];
-}
-
-// NaN and -infinity: -infinity (not eligible); +infinity: the largest float.
-__device__ __forceinline__ float clean_logit(float l)
-{
-    return l == l ? fminf(l, 3.402823466e38f) : -__builtin_huge_valf();
-}
-
-template <int CTRL>
-__device__ __forceinline__ float dpp(float x)
-{
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, false));
-}
-
-__device__ __forceinline__ float lane_value(float v, int lane)
-{
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
-}
-
-// Largest of the wave: four steps inside the rows of 16 lanes (quad_perm
-// [1,0,3,2] and [2,3,0,1], row_half_mirror, row_mirror), then the four rows.
-__device__ __forceinline__ float wave_max(float v)
-{
-    v = fmaxf(v, dpp<0xB1>(v));
-    v = fmaxf(v, dpp<0x4E>(v));
-    v = fmaxf(v, dpp<0x141>(v));
-    v = fmaxf(v, dpp<0x140>(v));
-    return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
-}
-
-__device__ __forceinline__ float wave_sum(float v)
-{
-    v += dpp<0xB1>(v);
-    v += dpp<0x4E>(v);
-    v += dpp<0x141>(v);
-    v += dpp<0x140>(v);
-    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
-}
-
-__device__ __forceinline__ double wave_sum(double v)
-{
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-    return v;
 }
 
 // The lane whose (key, id) is the wave's highest, ties to the lower id; -1 if
@@ -317,15 +267,6 @@ __global__ __launch_bounds__(kGateWaves* kWave) void k_gate(GateArgs a)
 // one over the gradient, in vectors of four experts where rows allow it.  8191
 // tokens, 256 experts, fp32: 7.8 us as a graph (9.9 with single stores), 2.2
 // TB/s; 8.3 to 8.5 us in a kernel trace.
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
-
 template <int VPL>
 __global__ __launch_bounds__(kGateWaves* kWave) void k_gate_backward(GateArgs a)
 {

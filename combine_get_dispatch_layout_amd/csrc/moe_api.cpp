@@ -7,6 +7,7 @@
 
 #include <cmath>
 
+#include "balance.hpp"
 #include "ep_host.hpp"
 #include "experts.hpp"
 
@@ -20,6 +21,7 @@ namespace {
     } while (0)
 
 constexpr int kMaxDim = 1 << 24;    // rows and columns of a weight matrix
+constexpr int kMaxInt8Cols = 1 << 17;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int64_t align_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
@@ -77,12 +79,57 @@ ep_status check_gate(const ep_gate_config* c, int64_t num_tokens, epk::GateArgs*
     return EP_OK;
 }
 
-// Checks a weight stack without its pointers (sizes only) or with them.
-ep_status check_weights(const ep_weights* w, const char* name, bool pointers)
+ep_status check_balance(const ep_balance_config* c, int64_t num_tokens, const int32_t* d_seq_start,
+                        int64_t num_sequences, epk::BalanceArgs* out)
+{
+    if (!c) return EP_FAIL(EP_ERR_INVALID_ARG, "config is NULL");
+    if (c->num_experts < 1 || c->num_experts > epk::kMaxExperts)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "num_experts=%d outside [1,%d]", c->num_experts,
+                       epk::kMaxExperts);
+    if (c->num_topk < 1 || c->num_topk > epk::kMaxTopk || c->num_topk > c->num_experts)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "num_topk=%d outside [1,%d] or above num_experts=%d",
+                       c->num_topk, epk::kMaxTopk, c->num_experts);
+    if (c->scoring != EP_SCORE_SOFTMAX && c->scoring != EP_SCORE_SIGMOID)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "scoring=%d unknown", c->scoring);
+    if (c->logits_type != EP_LOGITS_FP32 && c->logits_type != EP_LOGITS_BF16)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "logits_type=%d unknown", c->logits_type);
+    if (c->normalize != 0 && c->normalize != 1)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "normalize=%d must be 0 or 1", c->normalize);
+    if (!std::isfinite(c->coefficient)) return EP_FAIL(EP_ERR_INVALID_ARG, "coefficient is not finite");
+    if (num_tokens < 0 || num_tokens * c->num_topk >= (int64_t)1 << 31 || num_tokens >= (int64_t)1 << 31)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "num_tokens=%lld times num_topk=%d outside [0, 2^31)",
+                       (long long)num_tokens, c->num_topk);
+    if (num_sequences < 1 || num_sequences > EP_BALANCE_MAX_SEQUENCES)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "num_sequences=%lld outside [1,%d]", (long long)num_sequences,
+                       EP_BALANCE_MAX_SEQUENCES);
+    if (!d_seq_start && num_sequences != 1)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "%lld sequences need seq_start", (long long)num_sequences);
+    if (!aligned(d_seq_start, 4)) return EP_FAIL(EP_ERR_INVALID_ARG, "seq_start must be 4-byte aligned");
+    epk::BalanceArgs& a = *out;
+    a = epk::BalanceArgs{};
+    a.bf16 = c->logits_type == EP_LOGITS_BF16;
+    a.start = d_seq_start;
+    a.N = num_tokens;
+    a.E = c->num_experts;
+    a.K = c->num_topk;
+    a.Q = (int)num_sequences;
+    a.scoring = c->scoring;
+    a.normalize = c->normalize == 1;
+    a.k_magic = epk::div_magic((uint32_t)c->num_topk);
+    a.factor = (double)c->coefficient / (double)num_sequences * c->num_experts / c->num_topk;
+    return EP_OK;
+}
+
+// Checks a weight stack without its pointers (sizes only) or with them; int8:
+// of a call in 8-bit integers, which takes that format and no other.
+ep_status check_weights(const ep_weights* w, const char* name, bool pointers, bool int8 = false)
 {
     if (!w) return EP_FAIL(EP_ERR_INVALID_ARG, "%s is NULL", name);
-    if (w->format < EP_WEIGHT_BF16 || w->format > EP_WEIGHT_INT4)
+    if (w->format < EP_WEIGHT_BF16 || w->format > EP_WEIGHT_INT8)
         return EP_FAIL(EP_ERR_INVALID_ARG, "%s: format=%d unknown", name, w->format);
+    if (int8 != (w->format == EP_WEIGHT_INT8))
+        return EP_FAIL(EP_ERR_INVALID_ARG, "%s: ep_matmul and ep_expert_matmul take INT8 weights, the other "
+                       "products the other formats (format=%d)", name, w->format);
     if (w->num_experts < 1 || w->num_experts > epk::kMaxExperts)
         return EP_FAIL(EP_ERR_INVALID_ARG, "%s: num_experts=%d outside [1,%d]", name, w->num_experts,
                        epk::kMaxExperts);
@@ -94,6 +141,12 @@ ep_status check_weights(const ep_weights* w, const char* name, bool pointers)
         if (w->group != 0) return EP_FAIL(EP_ERR_INVALID_ARG, "%s: bf16 weights have no group", name);
         if (w->cols % 8 != 0)
             return EP_FAIL(EP_ERR_INVALID_ARG, "%s: cols=%d must be a multiple of 8", name, w->cols);
+    } else if (int8) {
+        if (w->group != 0) return EP_FAIL(EP_ERR_INVALID_ARG, "%s: INT8 weights have no group", name);
+        // (-128)^2 * cols has to fit the sums' 32 bits
+        if (w->cols % 16 != 0 || w->cols >= kMaxInt8Cols)
+            return EP_FAIL(EP_ERR_INVALID_ARG, "%s: cols=%d must be a multiple of 16 below %d", name, w->cols,
+                           kMaxInt8Cols);
     } else {
         const bool mx = w->format == EP_WEIGHT_MXFP4;
         if (mx ? w->group != 32 : (w->group != 32 && w->group != 64 && w->group != 128))
@@ -107,10 +160,10 @@ ep_status check_weights(const ep_weights* w, const char* name, bool pointers)
     if (!w->d_data || !aligned(w->d_data, 16))
         return EP_FAIL(EP_ERR_INVALID_ARG, "%s: data must be 16-byte aligned and not NULL", name);
     if (w->format == EP_WEIGHT_BF16 ? w->d_scales != nullptr
-                                    : (!w->d_scales || !aligned(w->d_scales, 16)))
+                                    : (!w->d_scales || !aligned(w->d_scales, int8 ? 4 : 16)))
         return EP_FAIL(EP_ERR_INVALID_ARG, "%s: scales must be %s", name,
                        w->format == EP_WEIGHT_BF16 ? "NULL for bf16 weights"
-                                                   : "16-byte aligned and not NULL");
+                       : int8 ? "4-byte aligned and not NULL" : "16-byte aligned and not NULL");
     if (w->d_zeros && w->format != EP_WEIGHT_INT4)
         return EP_FAIL(EP_ERR_INVALID_ARG, "%s: only INT4 weights have zeros", name);
     if (!aligned(w->d_zeros, 16))
@@ -125,11 +178,13 @@ epk::WeightArgs weight_args(const ep_weights* w)
     a.scales = static_cast<const uint8_t*>(w->d_scales);
     a.zeros = static_cast<const uint8_t*>(w->d_zeros);
     a.kind = w->format == EP_WEIGHT_BF16 ? epk::kBf16
+             : w->format == EP_WEIGHT_INT8 ? epk::kInt8
              : w->format == EP_WEIGHT_MXFP4 ? epk::kMxfp4
              : w->group == 32 ? epk::kInt4G32 : w->group == 64 ? epk::kInt4G64 : epk::kInt4G128;
     a.rows = w->rows;
-    a.cols = w->cols;
-    a.row_bytes = w->format == EP_WEIGHT_BF16 ? 2 * (int64_t)w->cols : w->cols / 2;
+    a.cols = a.kind == epk::kInt8 ? w->cols / 2 : w->cols;
+    a.row_bytes = a.kind == epk::kBf16 ? 2 * (int64_t)w->cols
+                  : a.kind == epk::kInt8 ? w->cols : w->cols / 2;
     a.row_groups = w->group ? w->cols / w->group : 0;
     return a;
 }
@@ -154,6 +209,73 @@ ep_status check_rows(const ep_weights* w, const void* d_x, int64_t rows, const v
     if (!d_x || !d_y) return EP_FAIL(EP_ERR_INVALID_ARG, "x or y is NULL");
     if (!aligned(d_x, 16) || !aligned(d_y, 2))
         return EP_FAIL(EP_ERR_INVALID_ARG, "x must be 16-byte aligned, y 2-byte aligned");
+    return EP_OK;
+}
+
+ep_status check_x_scales(const float* d_x_scales, int64_t rows)
+{
+    if (rows > 0 && (!d_x_scales || !aligned(d_x_scales, 4)))
+        return EP_FAIL(EP_ERR_INVALID_ARG, "x_scales must be 4-byte aligned and not NULL");
+    return EP_OK;
+}
+
+// A product with one matrix.
+ep_status check_dense(const ep_weights* w, bool int8, const void* d_x, int64_t num_rows, int32_t activation,
+                      void* d_y, epk::ProductArgs* out)
+{
+    ep_status st = check_weights(w, "w", true, int8);
+    if (st == EP_OK) st = check_activation(w, activation);
+    if (st == EP_OK) st = check_rows(w, d_x, num_rows, d_y);
+    if (st != EP_OK) return st;
+    if (w->num_experts != 1)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "%s takes one matrix (num_experts=%d)",
+                       int8 ? "ep_matmul" : "ep_matvec", w->num_experts);
+    epk::ProductArgs& a = *out;
+    a = epk::ProductArgs{};
+    a.w = weight_args(w);
+    a.E = 1;
+    a.units = activation == EP_ACT_SWIGLU ? w->rows / 2 : w->rows;
+    a.num_rows = num_rows;
+    a.x = static_cast<const uint16_t*>(d_x);
+    a.ldx = a.w.cols;
+    a.y = d_y;
+    a.ldy = a.units;
+    return EP_OK;
+}
+
+// A product of the rows that h's dispatch received with their experts' matrices.
+ep_status check_received(const ep_handle* h, const ep_weights* w, bool int8, const void* d_x, int64_t x_rows,
+                         int32_t activation, void* d_y, epk::ProductArgs* out)
+{
+    if (!h) return EP_FAIL(EP_ERR_INVALID_ARG, "handle is NULL");
+    ep_status st = check_weights(w, "w", true, int8);
+    if (st == EP_OK) st = check_activation(w, activation);
+    if (st == EP_OK) st = check_rows(w, d_x, x_rows, d_y);
+    if (st != EP_OK) return st;
+    const epk::HandleInfo info = epk::handle_info(h);
+    if (info.cfg->non_expand)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "non-expand rows belong to ranks, not experts");
+    if (w->num_experts != info.cfg->num_experts)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "w has %d experts, the handle %d", w->num_experts,
+                       info.cfg->num_experts);
+    if (info.num_tokens < 0) return EP_FAIL(EP_ERR_STATE, "ep_get_layout has not run on this handle");
+    if (info.pending)
+        return EP_FAIL(EP_ERR_STATE, "the handle's layout is waiting for ep_combine_overlap");
+    epk::ProductArgs& a = *out;
+    a = epk::ProductArgs{};
+    a.w = weight_args(w);
+    a.E = w->num_experts;
+    a.units = activation == EP_ACT_SWIGLU ? w->rows / 2 : w->rows;
+    a.num_rows = x_rows;
+    a.P = (int)(info.num_tokens * info.cfg->num_topk);
+    a.psum = info.psum_expert;
+    a.count = info.num_unaligned;
+    a.cap = info.cfg->expert_capacity;
+    a.x = static_cast<const uint16_t*>(d_x);
+    a.ldx = a.w.cols;
+    a.y = d_y;
+    a.ldy = a.units;
+    a.flags = info.flags;
     return EP_OK;
 }
 
@@ -249,24 +371,93 @@ ep_status ep_gate_backward(const ep_gate_config* cfg, const void* d_logits,
     return EP_OK;
 }
 
+ep_status ep_balance_workspace_size(const ep_balance_config* cfg, int64_t num_tokens,
+                                    int64_t num_sequences, int64_t* bytes)
+{
+    epk::BalanceArgs a;
+    static const int32_t some_start = 0;
+    ep_status st = check_balance(cfg, num_tokens, &some_start, num_sequences, &a);
+    if (st != EP_OK) return st;
+    if (!bytes) return EP_FAIL(EP_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = epk::carve_balance(num_tokens, a.E, a.Q).total;
+    return EP_OK;
+}
+
+ep_status ep_balance_loss(const ep_balance_config* cfg, const void* d_logits,
+                          const int32_t* d_topk_idx, const uint8_t* d_token_mask,
+                          int64_t num_tokens, const int32_t* d_seq_start, int64_t num_sequences,
+                          float* d_loss, int32_t* d_counts, int32_t* d_seq_tokens,
+                          float* d_score_sums, void* d_workspace, int64_t workspace_bytes,
+                          void* stream)
+{
+    epk::BalanceArgs a;
+    ep_status st = check_balance(cfg, num_tokens, d_seq_start, num_sequences, &a);
+    if (st != EP_OK) return st;
+    if (num_tokens > 0 && (!d_logits || !d_topk_idx))
+        return EP_FAIL(EP_ERR_INVALID_ARG, "logits or topk_idx is NULL");
+    if (!d_loss || !d_counts || !d_seq_tokens || !d_score_sums)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "loss, counts, seq_tokens or score_sums is NULL");
+    if (!aligned(d_logits, a.bf16 ? 2 : 4) || !aligned(d_topk_idx, 4) || !aligned(d_loss, 4) ||
+        !aligned(d_counts, 4) || !aligned(d_seq_tokens, 4) || !aligned(d_score_sums, 4))
+        return EP_FAIL(EP_ERR_INVALID_ARG, "logits, topk_idx or an output is not aligned to its type");
+    const epk::BalanceCarve c = epk::carve_balance(num_tokens, a.E, a.Q);
+    if (!d_workspace || !aligned(d_workspace, 256))
+        return EP_FAIL(EP_ERR_WORKSPACE, "workspace must be 256-byte aligned and not NULL");
+    if (workspace_bytes < c.total)
+        return EP_FAIL(EP_ERR_WORKSPACE, "workspace has %lld bytes, needs %lld",
+                       (long long)workspace_bytes, (long long)c.total);
+    unsigned char* ws = static_cast<unsigned char*>(d_workspace);
+    a.logits = d_logits;
+    a.vec = a.E % 4 == 0 && aligned(d_logits, a.bf16 ? 8 : 16);
+    a.topk = d_topk_idx;
+    a.mask = d_token_mask;
+    a.chunk = c.chunk;
+    a.slots = c.slots;
+    a.part_sum = reinterpret_cast<float*>(ws + c.sum);
+    a.part_count = reinterpret_cast<int32_t*>(ws + c.count);
+    a.part_tokens = reinterpret_cast<int32_t*>(ws + c.tokens);
+    a.part_loss = reinterpret_cast<double*>(ws + c.loss);
+    a.ticket = reinterpret_cast<uint32_t*>(ws + c.ticket);
+    a.loss = d_loss;
+    a.counts = d_counts;
+    a.tokens = d_seq_tokens;
+    a.sums = d_score_sums;
+    EP_HIP(epk::launch_balance(a, c, static_cast<hipStream_t>(stream)));
+    return EP_OK;
+}
+
+ep_status ep_balance_loss_backward(const ep_balance_config* cfg, const void* d_logits,
+                                   const uint8_t* d_token_mask, int64_t num_tokens,
+                                   const int32_t* d_seq_start, int64_t num_sequences,
+                                   const int32_t* d_counts, const int32_t* d_seq_tokens,
+                                   const float* d_grad_loss, void* d_grad_logits, void* stream)
+{
+    epk::BalanceArgs a;
+    ep_status st = check_balance(cfg, num_tokens, d_seq_start, num_sequences, &a);
+    if (st != EP_OK || num_tokens == 0) return st;
+    if (!d_logits || !d_counts || !d_seq_tokens || !d_grad_loss || !d_grad_logits)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "logits, counts, seq_tokens, grad_loss or grad_logits is NULL");
+    if (!aligned(d_logits, a.bf16 ? 2 : 4) || !aligned(d_grad_logits, a.bf16 ? 2 : 4) ||
+        !aligned(d_counts, 4) || !aligned(d_seq_tokens, 4) || !aligned(d_grad_loss, 4))
+        return EP_FAIL(EP_ERR_INVALID_ARG,
+                       "logits, counts, seq_tokens, grad_loss or grad_logits is not aligned to its type");
+    a.logits = d_logits;
+    a.vec = a.E % 4 == 0 && aligned(d_logits, a.bf16 ? 8 : 16) && aligned(d_grad_logits, a.bf16 ? 8 : 16);
+    a.mask = d_token_mask;
+    a.counts_in = d_counts;
+    a.tokens_in = d_seq_tokens;
+    a.grad_loss = d_grad_loss;
+    a.grad_logits = d_grad_logits;
+    EP_HIP(epk::launch_balance_backward(a, static_cast<hipStream_t>(stream)));
+    return EP_OK;
+}
+
 ep_status ep_matvec(const ep_weights* w, const void* d_x, int64_t num_rows, int32_t activation,
                     void* d_y, void* stream)
 {
-    ep_status st = check_weights(w, "w", true);
-    if (st == EP_OK) st = check_activation(w, activation);
-    if (st == EP_OK) st = check_rows(w, d_x, num_rows, d_y);
+    epk::ProductArgs a;
+    ep_status st = check_dense(w, false, d_x, num_rows, activation, d_y, &a);
     if (st != EP_OK) return st;
-    if (w->num_experts != 1)
-        return EP_FAIL(EP_ERR_INVALID_ARG, "ep_matvec takes one matrix (num_experts=%d)", w->num_experts);
-    epk::ProductArgs a = {};
-    a.w = weight_args(w);
-    a.E = 1;
-    a.units = activation == EP_ACT_SWIGLU ? w->rows / 2 : w->rows;
-    a.num_rows = num_rows;
-    a.x = static_cast<const uint16_t*>(d_x);
-    a.ldx = w->cols;
-    a.y = d_y;
-    a.ldy = a.units;
     EP_HIP(epk::launch_product(a, activation == EP_ACT_SWIGLU ? epk::kSwigluBf16 : epk::kStoreBf16,
                                static_cast<hipStream_t>(stream)));
     return EP_OK;
@@ -275,34 +466,36 @@ ep_status ep_matvec(const ep_weights* w, const void* d_x, int64_t num_rows, int3
 ep_status ep_expert_matvec(const ep_handle* h, const ep_weights* w, const void* d_x,
                            int64_t x_rows, int32_t activation, void* d_y, void* stream)
 {
-    if (!h) return EP_FAIL(EP_ERR_INVALID_ARG, "handle is NULL");
-    ep_status st = check_weights(w, "w", true);
-    if (st == EP_OK) st = check_activation(w, activation);
-    if (st == EP_OK) st = check_rows(w, d_x, x_rows, d_y);
+    epk::ProductArgs a;
+    ep_status st = check_received(h, w, false, d_x, x_rows, activation, d_y, &a);
     if (st != EP_OK) return st;
-    const epk::HandleInfo info = epk::handle_info(h);
-    if (info.cfg->non_expand)
-        return EP_FAIL(EP_ERR_INVALID_ARG, "non-expand rows belong to ranks, not experts");
-    if (w->num_experts != info.cfg->num_experts)
-        return EP_FAIL(EP_ERR_INVALID_ARG, "w has %d experts, the handle %d", w->num_experts,
-                       info.cfg->num_experts);
-    if (info.num_tokens < 0) return EP_FAIL(EP_ERR_STATE, "ep_get_layout has not run on this handle");
-    if (info.pending)
-        return EP_FAIL(EP_ERR_STATE, "the handle's layout is waiting for ep_combine_overlap");
-    epk::ProductArgs a = {};
-    a.w = weight_args(w);
-    a.E = w->num_experts;
-    a.units = activation == EP_ACT_SWIGLU ? w->rows / 2 : w->rows;
-    a.num_rows = x_rows;
-    a.P = (int)(info.num_tokens * info.cfg->num_topk);
-    a.psum = info.psum_expert;
-    a.count = info.num_unaligned;
-    a.cap = info.cfg->expert_capacity;
-    a.x = static_cast<const uint16_t*>(d_x);
-    a.ldx = w->cols;
-    a.y = d_y;
-    a.ldy = a.units;
-    a.flags = info.flags;
+    EP_HIP(epk::launch_product(a, activation == EP_ACT_SWIGLU ? epk::kSwigluBf16 : epk::kStoreBf16,
+                               static_cast<hipStream_t>(stream)));
+    return EP_OK;
+}
+
+ep_status ep_matmul(const ep_weights* w, const void* d_x, const float* d_x_scales,
+                    int64_t num_rows, int32_t activation, void* d_y, void* stream)
+{
+    epk::ProductArgs a;
+    ep_status st = check_dense(w, true, d_x, num_rows, activation, d_y, &a);
+    if (st == EP_OK) st = check_x_scales(d_x_scales, num_rows);
+    if (st != EP_OK) return st;
+    a.x_scales = d_x_scales;
+    EP_HIP(epk::launch_product(a, activation == EP_ACT_SWIGLU ? epk::kSwigluBf16 : epk::kStoreBf16,
+                               static_cast<hipStream_t>(stream)));
+    return EP_OK;
+}
+
+ep_status ep_expert_matmul(const ep_handle* h, const ep_weights* w, const void* d_x,
+                           const float* d_x_scales, int64_t x_rows, int32_t activation, void* d_y,
+                           void* stream)
+{
+    epk::ProductArgs a;
+    ep_status st = check_received(h, w, true, d_x, x_rows, activation, d_y, &a);
+    if (st == EP_OK) st = check_x_scales(d_x_scales, x_rows);
+    if (st != EP_OK) return st;
+    a.x_scales = d_x_scales;
     EP_HIP(epk::launch_product(a, activation == EP_ACT_SWIGLU ? epk::kSwigluBf16 : epk::kStoreBf16,
                                static_cast<hipStream_t>(stream)));
     return EP_OK;

@@ -32,6 +32,9 @@
 //   bf16:  8 columns, one matrix instruction per span;
 //   MXFP4: 32 columns = one scale group, four instructions.  Codes become
 //          bf16 with their scale in v_cvt_scalef32_pk_bf16_fp4 (exact);
+//   INT8:  16 columns, whose products with int8 rows of x go through
+//          v_mfma_i32_16x16x64_i8: the same bytes as bf16's 8 columns, exact
+//          sums, scaled by row and output before the store;
 //   INT4:  32 columns; the four words of the four lanes of a row are
 //          transposed in registers (v_permlane16_swap, v_permlane32_swap), so
 //          that instruction j covers the 32 consecutive columns of lane j.
@@ -61,12 +64,30 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// The same on 64 bytes of a row; the sums are whole numbers, held in the bits
+// of acc.
+__device__ __forceinline__ f32x4 mfma_i8(u32x4 a, u32x4 b, f32x4 c)
+{
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                                         __builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                                         __builtin_bit_cast(i32x4, c), 0, 0, 0));
+}
+
+// a + b of two such accumulators.
+template <int KIND>
+__device__ __forceinline__ f32x4 add_sums(f32x4 a, f32x4 b)
+{
+    if constexpr (KIND == kInt8)
+        return __builtin_bit_cast(f32x4, __builtin_bit_cast(i32x4, a) + __builtin_bit_cast(i32x4, b));
+    else return a + b;
 }
 
 __device__ __forceinline__ uint16_t to_bf16(float v)
@@ -115,15 +136,16 @@ __device__ __forceinline__ u32x4 load_weights(Buffer b, uint32_t lane_off, uint3
 
 template <int KIND>
 struct Format {
-    static constexpr bool kInt4 = KIND >= kInt4G32;
+    static constexpr bool kInt4 = is_int4(KIND);
+    static constexpr bool kPlain = is_plain(KIND);
     static constexpr int kLine = line_columns(KIND);
-    static constexpr int kParts = KIND == kBf16 ? 1 : 4;        // instructions of a span
+    static constexpr int kParts = kPlain ? 1 : 4;               // instructions of a span
     static constexpr int kGroup = KIND == kInt4G128 ? 128 : KIND == kInt4G64 ? 64 : 32;
     // INT4: parts of a span that share a scale
     static constexpr int kGroupParts = KIND == kInt4G128 ? 2 : 1;
     // bytes of x: a line, and from one span, part and lane c to the next
     static constexpr int kLineBytes = 2 * kLine;
-    static constexpr int kSpanBytes = KIND == kBf16 ? 16 : 64;
+    static constexpr int kSpanBytes = kPlain ? 16 : 64;
     static constexpr int kPartBytes = kInt4 ? 128 : 16;
     static constexpr int kLaneBytes = kInt4 ? 16 : KIND == kMxfp4 ? 128 : 32;
 };
@@ -132,8 +154,8 @@ struct Format {
 template <int KIND, int U>
 struct Scales {
     static constexpr int kGroups = U * 128 / Format<KIND>::kGroup;
-    static constexpr int kWords = KIND == kBf16 ? 0 : (KIND == kMxfp4 ? kGroups : 2 * kGroups) / 4;
-    static constexpr int kZeroWords = KIND <= kMxfp4 ? 0 : (kGroups + 3) / 4;
+    static constexpr int kWords = is_plain(KIND) ? 0 : (KIND == kMxfp4 ? kGroups : 2 * kGroups) / 4;
+    static constexpr int kZeroWords = !is_int4(KIND) ? 0 : (kGroups + 3) / 4;
     uint32_t s[kWords > 0 ? kWords : 1];
     uint32_t z[kZeroWords > 0 ? kZeroWords : 1];
 };
@@ -228,7 +250,7 @@ __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b)
 template <int KIND>
 __device__ __forceinline__ void expand(u32x4 f, const SpanScale<KIND>& s, u32x4 (&b)[Format<KIND>::kParts])
 {
-    if constexpr (KIND == kBf16) {
+    if constexpr (is_plain(KIND)) {
         b[0] = f;
     } else if constexpr (KIND == kMxfp4) {
 #pragma unroll
@@ -262,7 +284,9 @@ __device__ __forceinline__ void multiply(const u32x4 (&b)[Format<KIND>::kParts],
                                          f32x4& acc)
 {
     using F = Format<KIND>;
-    if constexpr (!F::kInt4) {
+    if constexpr (KIND == kInt8) {
+        acc = mfma_i8(x[0], b[0], acc);
+    } else if constexpr (!F::kInt4) {
 #pragma unroll
         for (int j = 0; j < F::kParts; ++j) {
             acc = mfma(x[j], b[j], acc);
@@ -463,7 +487,7 @@ constexpr int kListRows = 128;      // ... and their rows, at most
 // block in private memory (272 bytes a lane), so the loads ahead gain little
 // there: 64 tokens, 8 experts, 4096 x 14336, INT4: 977 us for a floor of 100.
 template <int KIND, int EPI, int TT, bool DIRECT, int kU, int kWaves>
-__global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kWaves == 4 ? (KIND <= kMxfp4 ? 3 : 2) : kWaves / 4) void k_product(ProductArgs a)
+__global__ __launch_bounds__(kWaves* kWave, TT == 2 && is_int4(KIND) ? 1 : kWaves == 4 ? (is_int4(KIND) ? 2 : 3) : kWaves / 4) void k_product(ProductArgs a)
 {
     constexpr int kThreads = kWaves * kWave;
     using F = Format<KIND>;
@@ -592,7 +616,7 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
                 for (int v = 0; v < 2; ++v)
                     data_off[r][v] = (uint32_t)min(8 * v + (lane & 7), have - 1) * (uint32_t)row_bytes +
                                      16u * (lane >> 3);
-                if constexpr (KIND != kBf16) {
+                if constexpr (!F::kPlain) {
                     scales[r] = make_buffer(a.w.scales + first * row_groups * kScaleBytes,
                                             there ? (int64_t)have * row_groups * kScaleBytes : 0);
                     scale_off[r] = (uint32_t)min(n, have - 1) * (uint32_t)(row_groups * kScaleBytes);
@@ -608,7 +632,7 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
         };
         auto load_scales = [&](int r, int block, Scales<KIND, kU>& o) {
             constexpr uint32_t kG = Scales<KIND, kU>::kGroups;
-            if constexpr (KIND != kBf16)
+            if constexpr (!F::kPlain)
                 load_words<Scales<KIND, kU>::kWords>(o.s, scales[r], scale_off[r], block * kG * kScaleBytes);
             if constexpr (F::kInt4) {
                 if (has_zeros) {
@@ -738,6 +762,7 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
 #pragma unroll
                 for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
             int unit0 = 0;
+            [[maybe_unused]] float ws[RT], xs[TT][4];
             // A operands of a span; x0: the ones that were loaded ahead, if any
             auto x_of = [&](int t, int line, int v, bool partial, u32x4 (*x0)[kPlanes * kParts],
                             u32x4 (&x)[kPlanes * kParts]) {
@@ -792,6 +817,21 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
                     }
                 }
                 unit0 = unit_of(tile, seg);
+                if constexpr (KIND == kInt8) {
+                    // scales of this lane's outputs and rows, for the store
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const int u = min(unit0 + (kGate ? 0 : 16 * r) + n, a.units - 1);
+                        ws[r] = reinterpret_cast<const float*>(a.w.scales)[expert_row + (kGate && r == 1 ? a.units : 0) + u];
+                    }
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int m = 16 * t + 4 * c + i;
+                            xs[t][i] = m < rows ? a.x_scales[list[first_row + m]] : 0.f;
+                        }
+                }
                 for (int j = 0; j < mine; ++j) {
                     const int line0 = (kq + j * kw) * kL;
                     // the block after this one: of this tile, of the next, or none
@@ -899,11 +939,20 @@ __global__ __launch_bounds__(kWaves* kWave, TT == 2 && KIND >= kInt4G32 ? 1 : kW
                         for (int r = 0; r < RT; ++r)
 #pragma unroll
                             for (int t = 0; t < TT; ++t)
-                                acc[r][t] += mine_red[(((wave + q) * RT + r) * TT + t) * kWave + lane];
+                                acc[r][t] = add_sums<KIND>(acc[r][t], mine_red[(((wave + q) * RT + r) * TT + t) * kWave + lane]);
             }
 
             // ---- store: this lane has output n of rows 4c .. 4c+3 of each tile
             if (kq == 0 && here) {
+                if constexpr (KIND == kInt8) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int t = 0; t < TT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                acc[r][t][i] = (float)__builtin_bit_cast(i32x4, acc[r][t])[i] * xs[t][i] * ws[r];
+                }
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
 #pragma unroll

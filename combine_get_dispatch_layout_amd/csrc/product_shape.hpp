@@ -7,12 +7,18 @@
 namespace epk {
 
 // Storage formats as the kernels are instantiated for them.
-enum WeightKind { kBf16 = 0, kMxfp4 = 1, kInt4G32 = 2, kInt4G64 = 3, kInt4G128 = 4 };
+enum WeightKind { kBf16 = 0, kMxfp4 = 1, kInt4G32 = 2, kInt4G64 = 3, kInt4G128 = 4, kInt8 = 5 };
+
+constexpr bool is_int4(int kind) { return kind >= kInt4G32 && kind <= kInt4G128; }
+
+// Formats whose bytes go to the matrix cores as they are.  Of kInt8 two columns
+// count as one here and in product.hpp, so that it has bf16's sizes throughout.
+constexpr bool is_plain(int kind) { return kind == kBf16 || kind == kInt8; }
 
 namespace prod {
 
 // Columns of a line (128 bytes of a weight row).
-constexpr int line_columns(int kind) { return kind == kBf16 ? 64 : 256; }
+constexpr int line_columns(int kind) { return is_plain(kind) ? 64 : 256; }
 
 // Bytes of a row of x in LDS: whole lines, and 16 so that rows start in
 // different banks.
@@ -36,12 +42,12 @@ constexpr int64_t sums_bytes(int waves, int kw, int tt)
 // where x (from memory) or the scales take more registers.
 constexpr int spans_ahead(int kind, bool direct)
 {
-    return direct ? (kind == kBf16 ? 4 : 2) : (kind == kInt4G32 ? 2 : 4);
+    return direct ? (is_plain(kind) ? 4 : 2) : (kind == kInt4G32 ? 2 : 4);
 }
 constexpr int kSpansSmall = 2;
 
 // INT4 with two row tiles needs more than the 256 registers of eight waves.
-constexpr int two_tile_waves(int kind) { return kind >= kInt4G32 ? 4 : 8; }
+constexpr int two_tile_waves(int kind) { return is_int4(kind) ? 4 : 8; }
 
 // Waves of the big blocks (one of eight waves a CU) that run at a time.
 constexpr int64_t kAtOnce = 2048;
@@ -88,7 +94,7 @@ inline Shape choose_shape(int kind, bool gate, int planes, int64_t cols, int64_t
     const int64_t passes = experts * ((likely + 16 * tt - 1) / (16 * tt));
     s.tiles = passes * ((units + (gate ? 15 : 31)) / (gate ? 16 : 32));
     const int64_t stride = planes * x_stride(kind, cols);
-    const int64_t row_bytes = kind == kBf16 ? 2 * cols : cols / 2;
+    const int64_t row_bytes = is_plain(kind) ? 2 * cols : cols / 2;
     // waves of a team: as long as all waves' work fits the GPU at once
     auto waves_per_tile = [&](int most, int spans, int64_t at_once) {
         const int64_t blocks = (row_bytes / 64 + spans - 1) / spans;

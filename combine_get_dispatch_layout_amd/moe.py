@@ -1,14 +1,14 @@
-"""Thin Python binding of the calls of include/ep_moe.h (router, products with
-expert weights, whole expert layer), over torch tensors.
+"""Thin Python binding of the calls of include/ep_moe.h (router and its balance
+loss, products with expert weights, whole expert layer), over torch tensors.
 
 As in ep.py: argument marshalling only, the functions carry the C names, the
 work is queued on the current stream of the tensors' device, and outputs are
-allocated with torch when none are passed.  ep_gate alone takes part in
-autograd; the other calls' outputs have no gradient.
+allocated with torch when none are passed.  ep_gate and ep_balance_loss take
+part in autograd; the other calls' outputs have no gradient.
 """
 import ctypes
 from dataclasses import dataclass, field
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -17,19 +17,27 @@ from .ep import EP_OK, Handle, _check, lib
 
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 EP_LOGITS_FP32, EP_LOGITS_BF16 = 0, 1
-EP_WEIGHT_BF16, EP_WEIGHT_MXFP4, EP_WEIGHT_INT4 = 0, 1, 2
+EP_WEIGHT_BF16, EP_WEIGHT_MXFP4, EP_WEIGHT_INT4, EP_WEIGHT_INT8 = 0, 1, 2, 3
 EP_ACT_NONE, EP_ACT_SWIGLU = 0, 1
 EP_MOE_MAX_TOKENS = 256
+EP_BALANCE_MAX_SEQUENCES = 1 << 18
 
 # Every symbol include/ep_moe.h declares.
-SYMBOLS = ("ep_gate", "ep_gate_backward", "ep_matvec", "ep_expert_matvec",
-           "ep_moe_workspace_size", "ep_moe_layer")
+SYMBOLS = ("ep_gate", "ep_gate_backward", "ep_balance_workspace_size", "ep_balance_loss",
+           "ep_balance_loss_backward", "ep_matvec", "ep_expert_matvec", "ep_matmul",
+           "ep_expert_matmul", "ep_moe_workspace_size", "ep_moe_layer")
 
 
 class ep_gate_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("num_experts", "num_topk", "scoring", "renormalize", "num_groups", "topk_groups",
                  "group_top", "group_limit", "logits_type")] + [("scale", ctypes.c_float)]
+
+
+class ep_balance_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("num_experts", "num_topk", "scoring", "normalize", "logits_type")] + \
+               [("coefficient", ctypes.c_float)]
 
 
 class ep_weights(ctypes.Structure):
@@ -52,6 +60,11 @@ def _lib():
         L.ep_gate_backward.argtypes = [P, P, P, P, I64, P, P]
         L.ep_matvec.argtypes = [P, P, I64, I32, P, P]
         L.ep_expert_matvec.argtypes = [P, P, P, I64, I32, P, P]
+        L.ep_balance_workspace_size.argtypes = [P, I64, I64, P]
+        L.ep_balance_loss.argtypes = [P, P, P, P, I64, P, I64, P, P, P, P, P, I64, P]
+        L.ep_balance_loss_backward.argtypes = [P, P, P, I64, P, I64, P, P, P, P, P]
+        L.ep_matmul.argtypes = [P, P, P, I64, I32, P, P]
+        L.ep_expert_matmul.argtypes = [P, P, P, P, I64, I32, P, P]
         L.ep_moe_workspace_size.argtypes = [P, P, P, I64, P]
         L.ep_moe_layer.argtypes = [P, P, P, P, P, P, I64, P, P, I64, P]
         for name in SYMBOLS:
@@ -203,6 +216,157 @@ def ep_gate_backward(cfg: GateConfig, logits: torch.Tensor, topk_idx: torch.Tens
     return grad_logits
 
 
+# ---- balance loss --------------------------------------------------------------
+
+
+@dataclass(frozen=True)
+class BalanceConfig:
+    num_experts: int
+    num_topk: int
+    scoring: int = EP_SCORE_SOFTMAX
+    normalize: bool = True
+    coefficient: float = 1.0
+    _c: dict = field(init=False, repr=False, compare=False)
+
+    def __post_init__(self):
+        make = lambda kind: ep_balance_config(  # noqa: E731
+            self.num_experts, self.num_topk, self.scoring, int(bool(self.normalize)), kind,
+            self.coefficient)
+        object.__setattr__(self, "_c", {torch.float32: make(EP_LOGITS_FP32),
+                                        torch.bfloat16: make(EP_LOGITS_BF16)})
+
+    def c(self, dtype):
+        return ctypes.byref(self._c[dtype])
+
+
+class Balance(NamedTuple):
+    """What ep_balance_loss returns."""
+    loss: torch.Tensor          # fp32 []
+    counts: torch.Tensor        # int32 [Q, E]
+    seq_tokens: torch.Tensor    # int32 [Q]
+    score_sums: torch.Tensor    # fp32 [Q, E]
+
+
+def ep_balance_workspace_size(cfg: BalanceConfig, num_tokens: int, num_sequences: int = 1) -> int:
+    out = ctypes.c_int64()
+    _check(_lib().ep_balance_workspace_size(cfg.c(torch.float32), num_tokens, num_sequences,
+                                            ctypes.byref(out)))
+    return out.value
+
+
+def _check_sequences(seq_start, device):
+    """Number of sequences."""
+    if seq_start is None:
+        return 1
+    if (seq_start.dtype != torch.int32 or seq_start.dim() != 1 or seq_start.numel() < 2
+            or seq_start.device != device):
+        raise ValueError(f"seq_start must be int32 [sequences + 1] on {device}")
+    return seq_start.numel() - 1
+
+
+class _BalanceLoss(torch.autograd.Function):
+    """ep_balance_loss with ep_balance_loss_backward as the loss's gradient."""
+
+    @staticmethod
+    def forward(ctx, cfg, logits, topk_idx, token_mask, seq_start, loss, counts, seq_tokens,
+                score_sums, workspace):
+        out = ep_balance_loss(cfg, logits, topk_idx, token_mask, seq_start, loss, counts, seq_tokens,
+                              score_sums, workspace)
+        ctx.cfg, ctx.leaf = cfg, logits.is_leaf
+        # a given buffer may be filled again before the backward pass
+        ctx.save_for_backward(logits, token_mask, seq_start,
+                              out.counts if counts is None else out.counts.clone(),
+                              out.seq_tokens if seq_tokens is None else out.seq_tokens.clone())
+        # outputs of their own, in the given memory: the buffers keep no graph
+        out = [o if given is None else o.detach()
+               for o, given in zip(out, (loss, counts, seq_tokens, score_sums))]
+        ctx.mark_non_differentiable(*out[1:])
+        ctx.set_materialize_grads(False)
+        return tuple(out)
+
+    @staticmethod
+    def backward(ctx, grad_loss, *_):
+        if grad_loss is None:
+            return (None,) * 10
+        if torch.is_grad_enabled():     # create_graph: would lose the second order silently
+            raise RuntimeError("ep_balance_loss has a first order gradient only")
+        # a leaf's gradient accumulates on the stream of its first use, which a
+        # captured backward pass must not touch
+        if ctx.leaf and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the backward pass of ep_balance_loss into leaf logits must not be "
+                               "captured: capture ep_balance_loss_backward")
+        logits, token_mask, seq_start, counts, seq_tokens = ctx.saved_tensors
+        grad = ep_balance_loss_backward(ctx.cfg, logits, counts, seq_tokens, grad_loss.contiguous(),
+                                        token_mask, seq_start)
+        return (None, grad) + (None,) * 8
+
+
+def ep_balance_loss(cfg: BalanceConfig, logits: torch.Tensor, topk_idx: torch.Tensor,
+                    token_mask: Optional[torch.Tensor] = None,
+                    seq_start: Optional[torch.Tensor] = None, loss: Optional[torch.Tensor] = None,
+                    counts: Optional[torch.Tensor] = None, seq_tokens: Optional[torch.Tensor] = None,
+                    score_sums: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> Balance:
+    """Per-expert counts of the routing topk_idx int32 [N, K] and the balance
+    loss of the logits [N, E] (fp32 or bf16).  token_mask bool / uint8 [N]: rows
+    with 0 do not count; seq_start int32 [Q+1]: the sequences' bounds (default:
+    the batch is one).  Returns Balance(loss [], counts [Q, E], seq_tokens [Q],
+    score_sums [Q, E]).  Where autograd records and the logits require a
+    gradient, the returned loss has one (a loss passed in is filled, but it is
+    the returned tensor that has the gradient).  workspace: uint8, at least
+    ep_balance_workspace_size bytes (allocated for this call when not given)."""
+    if logits.requires_grad and torch.is_grad_enabled():
+        return Balance(*_BalanceLoss.apply(cfg, logits, topk_idx, token_mask, seq_start, loss, counts,
+                                           seq_tokens, score_sums, workspace))
+    N, dev = _check_logits(cfg, logits)
+    Q = _check_sequences(seq_start, dev)
+    _check_tensor("topk_idx", topk_idx, (torch.int32,), (N, cfg.num_topk), dev)
+    _check_tensor("token_mask", token_mask, (torch.bool, torch.uint8), (N,), dev)
+
+    def output(name, given, dtype, shape):
+        if given is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        _check_tensor(name, given, (dtype,), shape, dev)
+        return given
+
+    E = cfg.num_experts
+    loss = output("loss", loss, torch.float32, ())
+    counts = output("counts", counts, torch.int32, (Q, E))
+    seq_tokens = output("seq_tokens", seq_tokens, torch.int32, (Q,))
+    score_sums = output("score_sums", score_sums, torch.float32, (Q, E))
+    if workspace is None:
+        workspace = torch.empty(ep_balance_workspace_size(cfg, N, Q), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError("workspace must be on the logits' device")
+    _call(dev, _lib().ep_balance_loss, cfg.c(logits.dtype), _ptr(logits), _ptr(topk_idx),
+          _ptr(token_mask), N, _ptr(seq_start), Q, _ptr(loss), _ptr(counts), _ptr(seq_tokens),
+          _ptr(score_sums), _ptr(workspace), workspace.numel() * workspace.element_size())
+    return Balance(loss, counts, seq_tokens, score_sums)
+
+
+def ep_balance_loss_backward(cfg: BalanceConfig, logits: torch.Tensor, counts: torch.Tensor,
+                             seq_tokens: torch.Tensor, grad_loss: torch.Tensor,
+                             token_mask: Optional[torch.Tensor] = None,
+                             seq_start: Optional[torch.Tensor] = None,
+                             grad_logits: Optional[torch.Tensor] = None):
+    """Gradient of ep_balance_loss's loss with respect to the logits, given its
+    counts and seq_tokens (or their sums over ranks): grad_logits [N, E] of the
+    logits' type."""
+    N, dev = _check_logits(cfg, logits)
+    Q = _check_sequences(seq_start, dev)
+    _check_tensor("counts", counts, (torch.int32,), (Q, cfg.num_experts), dev)
+    _check_tensor("seq_tokens", seq_tokens, (torch.int32,), (Q,), dev)
+    _check_tensor("grad_loss", grad_loss, (torch.float32,), (), dev)
+    _check_tensor("token_mask", token_mask, (torch.bool, torch.uint8), (N,), dev)
+    if grad_logits is None:
+        grad_logits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    else:
+        _check_tensor("grad_logits", grad_logits, (logits.dtype,), logits.shape, dev)
+    _call(dev, _lib().ep_balance_loss_backward, cfg.c(logits.dtype), _ptr(logits), _ptr(token_mask), N,
+          _ptr(seq_start), Q, _ptr(counts), _ptr(seq_tokens), _ptr(grad_loss), _ptr(grad_logits))
+    return grad_logits
+
+
 # ---- products with expert weights --------------------------------------------
 
 
@@ -211,21 +375,29 @@ class Weights:
     its tensors alive.  data: bf16 [E, rows, cols], or uint8 [E, rows, cols/2]
     (two codes a byte, column 2i in the low nibble) with scales
     [E, rows, cols/group]: uint8 E8M0 (MXFP4) or bf16 (INT4, optionally with
-    uint8 zeros).  A missing first dimension stands for one matrix."""
+    uint8 zeros), or int8 [E, rows, cols] with fp32 scales [E, rows] (INT8).  A
+    missing first dimension stands for one matrix."""
 
     def __init__(self, format: int, data: torch.Tensor, scales: Optional[torch.Tensor] = None,
                  zeros: Optional[torch.Tensor] = None, group: int = 0):
-        if format not in (EP_WEIGHT_BF16, EP_WEIGHT_MXFP4, EP_WEIGHT_INT4):
+        if format not in (EP_WEIGHT_BF16, EP_WEIGHT_MXFP4, EP_WEIGHT_INT4, EP_WEIGHT_INT8):
             raise ValueError(f"unknown weight format {format}")
-        want = torch.bfloat16 if format == EP_WEIGHT_BF16 else torch.uint8
+        want = {EP_WEIGHT_BF16: torch.bfloat16, EP_WEIGHT_INT8: torch.int8}.get(format, torch.uint8)
+        per = 2 if want == torch.uint8 else 1       # columns of an element
         if data.dtype != want or data.dim() not in (2, 3):
-            raise ValueError(f"data must be {want} [E, rows, cols{'/2' if format else ''}]")
+            raise ValueError(f"data must be {want} [E, rows, cols{'/2' if per == 2 else ''}]")
         stack = data if data.dim() == 3 else data[None]
         E, M = stack.shape[:2]
-        C = stack.shape[2] * (2 if format else 1)
+        C = stack.shape[2] * per
         if format == EP_WEIGHT_BF16:
             if scales is not None or zeros is not None or group:
                 raise ValueError("bf16 weights have no scales, zeros or group")
+        elif format == EP_WEIGHT_INT8:
+            if zeros is not None or group:
+                raise ValueError("INT8 weights have no zeros or group")
+            if scales is None:
+                raise ValueError("INT8 weights need scales")
+            _check_tensor("scales", scales, (torch.float32,), data.shape[:-1], data.device)
         else:
             group = group or (32 if format == EP_WEIGHT_MXFP4 else 0)
             if group <= 0 or C % group:
@@ -247,13 +419,14 @@ class Weights:
         self._ref = ctypes.byref(self._c)
 
 
-def _check_product(w, x, y, activation):
+def _check_product(w, x, y, activation, dtype=torch.bfloat16):
     if activation not in (EP_ACT_NONE, EP_ACT_SWIGLU):
         raise ValueError(f"unknown activation {activation}")
     if activation == EP_ACT_SWIGLU and w.rows % 2:
         raise ValueError("SWIGLU needs an even number of weight rows")
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != w.cols or x.device != w.device:
-        raise ValueError(f"x must be bf16 [rows, {w.cols}] on {w.device}")
+    if x.dtype != dtype or x.dim() != 2 or x.shape[1] != w.cols or x.device != w.device:
+        raise ValueError(f"x must be {'bf16' if dtype == torch.bfloat16 else 'int8'} [rows, {w.cols}] "
+                         f"on {w.device}")
     shape = (x.shape[0], w.rows // 2 if activation else w.rows)
     if y is None:
         return torch.empty(shape, dtype=torch.bfloat16, device=x.device)
@@ -278,6 +451,39 @@ def ep_expert_matvec(h: Handle, w: Weights, x: torch.Tensor, y: Optional[torch.T
         raise ValueError("x must be on the handle's device")
     y = _check_product(w, x, y, activation)
     _call(x.device, _lib().ep_expert_matvec, h.ptr, w._ref, _ptr(x), x.shape[0], activation, _ptr(y))
+    return y
+
+
+def _check_x_scales(x, x_scales):
+    """[rows], or the [rows, 1] of a dispatch's recv_scales."""
+    if x_scales.dim() == 2:
+        _check_tensor("x_scales", x_scales, (torch.float32,), (x.shape[0], 1), x.device)
+    else:
+        _check_tensor("x_scales", x_scales, (torch.float32,), (x.shape[0],), x.device)
+
+
+def ep_matmul(w: Weights, x: torch.Tensor, x_scales: torch.Tensor, y: Optional[torch.Tensor] = None,
+              activation: int = EP_ACT_NONE):
+    """y bf16 = act((x W^T) * x_scales * w's scales) in 8-bit integers, for x
+    int8 [rows, cols] with x_scales fp32 [rows] or [rows, 1] and one matrix
+    (INT8 weights)."""
+    y = _check_product(w, x, y, activation, torch.int8)
+    _check_x_scales(x, x_scales)
+    _call(x.device, _lib().ep_matmul, w._ref, _ptr(x), _ptr(x_scales), x.shape[0], activation, _ptr(y))
+    return y
+
+
+def ep_expert_matmul(h: Handle, w: Weights, x: torch.Tensor, x_scales: torch.Tensor,
+                     y: Optional[torch.Tensor] = None, activation: int = EP_ACT_NONE):
+    """The same for x in the receive-row order of h's layout (an int8
+    dispatch's recv_x and recv_scales), each row with its expert's matrix.  Rows
+    without a token are not written (left unset in a y allocated here)."""
+    if h.device != x.device:
+        raise ValueError("x must be on the handle's device")
+    y = _check_product(w, x, y, activation, torch.int8)
+    _check_x_scales(x, x_scales)
+    _call(x.device, _lib().ep_expert_matmul, h.ptr, w._ref, _ptr(x), _ptr(x_scales), x.shape[0],
+          activation, _ptr(y))
     return y
 
 

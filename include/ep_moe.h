@@ -9,8 +9,13 @@
  *   ep_expert_matvec    products of the received rows of a dispatch with
  *                       their experts' matrices (between ep_dispatch and
  *                       ep_combine)
+ *   ep_matmul,          the same in 8-bit integers on both sides, for any
+ *   ep_expert_matmul    number of rows: rows as an int8 dispatch delivers
+ *                       them, with a scale for each row and each output
  *   ep_moe_layer        the whole expert layer for a few tokens, from
  *                       topk_idx to the combined output, without the shuffle
+ *   ep_balance_loss     per-expert counts of a routing and the balance loss,
+ *                       and ep_balance_loss_backward, its gradient
  *
  * The conventions of ep.h hold for every call: d_* are device pointers of
  * the current HIP device, the caller owns all memory, `stream` is a
@@ -82,6 +87,67 @@ ep_status ep_gate_backward(const ep_gate_config* cfg, const void* d_logits,
                            const int32_t* d_topk_idx, const float* d_grad_weights,
                            int64_t num_tokens, void* d_grad_logits, void* stream);
 
+/* ---- balance loss --------------------------------------------------------- */
+
+typedef struct ep_balance_config {
+    int32_t num_experts;   /* E: 1..1024                                       */
+    int32_t num_topk;      /* K: 1..16, at most E                              */
+    int32_t scoring;       /* EP_SCORE_*                                       */
+    int32_t normalize;     /* sigmoid: 1 = divided by their sum over all experts;
+                              a softmax is so in any case                      */
+    int32_t logits_type;   /* EP_LOGITS_*                                      */
+    float coefficient;     /* of the loss, finite                              */
+} ep_balance_config;
+
+/* Sequences of one call, at most. */
+#define EP_BALANCE_MAX_SEQUENCES (1 << 18)
+
+/* Bytes of device workspace that ep_balance_loss needs. */
+ep_status ep_balance_workspace_size(const ep_balance_config* cfg, int64_t num_tokens,
+                                    int64_t num_sequences, int64_t* bytes);
+
+/* Counts of a routing and the loss that keeps experts evenly used.  With V_q the
+ * unmasked tokens of sequence q, T_q their number and p their scores:
+ *   d_counts int32 [Q, E]: entries of V_q's topk_idx rows that name the expert;
+ *   d_seq_tokens int32 [Q]: T_q;
+ *   d_score_sums fp32 [Q, E]: sum over V_q of p[t, e];
+ *   d_loss fp32 [1]: coefficient / Q * sum over q with T_q > 0 of
+ *     E / (K * T_q^2) * sum over e of counts[q, e] * score_sums[q, e],
+ *   coefficient for a sequence that uses its experts evenly.
+ *   d_logits [num_tokens, E]; d_topk_idx int32 [num_tokens, K], ep_gate's or any:
+ *   ids outside [0, E) are not counted, an id listed twice counts twice;
+ *   d_token_mask uint8 [num_tokens] or NULL: tokens with 0 (padding) are no part
+ *   of their sequence.
+ *   d_seq_start int32 [Q+1], not decreasing: sequence q is tokens [start[q],
+ *   start[q+1]); tokens before the first and behind the last belong to none, a
+ *   sequence may be empty.  Starts outside [0, num_tokens] count as the nearer
+ *   end; decreasing ones give unspecified values.  NULL: the batch is one
+ *   sequence (Q == 1).
+ *   An expert whose logit is NaN or -infinity has score 0; a logit of +infinity
+ *   counts as the largest finite fp32.
+ *   num_tokens * K below 2^31.  Scores are summed in fp32 over at most 1024
+ *   tokens, then in fp64; no result depends on the order in which blocks run.
+ *   d_workspace: 256-byte aligned, needs no clearing; in use by one stream (or
+ *   graph in flight) at a time. */
+ep_status ep_balance_loss(const ep_balance_config* cfg, const void* d_logits,
+                          const int32_t* d_topk_idx, const uint8_t* d_token_mask,
+                          int64_t num_tokens, const int32_t* d_seq_start, int64_t num_sequences,
+                          float* d_loss, int32_t* d_counts, int32_t* d_seq_tokens,
+                          float* d_score_sums, void* d_workspace, int64_t workspace_bytes,
+                          void* stream);
+
+/* Gradient of that loss with respect to the logits, the choice (so the counts)
+ * held fixed: d_grad_logits [num_tokens, E], of the logits' type, written whole;
+ * tokens that are masked or of no sequence get 0, as do experts without a score.
+ *   d_counts, d_seq_tokens: ep_balance_loss's, or their sums over the ranks that
+ *   share a batch.  d_grad_loss fp32 [1].  Logits, mask, starts and
+ *   num_sequences as there. */
+ep_status ep_balance_loss_backward(const ep_balance_config* cfg, const void* d_logits,
+                                   const uint8_t* d_token_mask, int64_t num_tokens,
+                                   const int32_t* d_seq_start, int64_t num_sequences,
+                                   const int32_t* d_counts, const int32_t* d_seq_tokens,
+                                   const float* d_grad_loss, void* d_grad_logits, void* stream);
+
 /* ---- products with expert weights --------------------------------------- */
 
 enum {
@@ -92,13 +158,16 @@ enum {
                               columns [E, rows, cols/32]; 255 is NaN.  An
                               element is rounded to bf16, which is exact from
                               2^-126 to the largest bf16                       */
-    EP_WEIGHT_INT4 = 2     /* d_data two codes a byte as above; an element is
+    EP_WEIGHT_INT4 = 2,    /* d_data two codes a byte as above; an element is
                               (code - zero) * scale, with d_scales bf16
                               [E, rows, cols/group] and d_zeros uint8 of that
                               shape holding 0..15, or NULL: every zero is 8.
                               Multiplied as (16 + code) - (16 + zero): no sum of
                               a group overflows for |x| up to 2^116; an infinity
                               in x makes NaN                                   */
+    EP_WEIGHT_INT8 = 3     /* for ep_matmul and ep_expert_matmul alone: d_data
+                              int8 [E, rows, cols], cols % 16 == 0 and below
+                              2^17; d_scales fp32 [E, rows], 4-byte aligned    */
 };
 
 /* Applied to a product's rows. */
@@ -112,11 +181,11 @@ enum {
 #define EP_MOE_MAX_TOKENS 256
 
 /* A stack of weight matrices, row-major, contiguous, in caller-owned device
- * memory, each 16-byte aligned. */
+ * memory, each 16-byte aligned (but INT8's scales). */
 typedef struct ep_weights {
     int32_t format;        /* EP_WEIGHT_*                                      */
-    int32_t group;         /* columns per scale: 0 (BF16), 32 (MXFP4), 32, 64 or
-                              128 (INT4); divides cols                         */
+    int32_t group;         /* columns per scale: 0 (BF16, INT8), 32 (MXFP4), 32,
+                              64 or 128 (INT4); divides cols                   */
     int32_t num_experts;   /* E: 1..1024                                       */
     int32_t rows;          /* M: outputs, 1..2^24                              */
     int32_t cols;          /* C: inputs, up to 2^24                            */
@@ -152,6 +221,25 @@ ep_status ep_matvec(const ep_weights* w, const void* d_x, int64_t num_rows, int3
  *   rows belong to ranks). */
 ep_status ep_expert_matvec(const ep_handle* h, const ep_weights* w, const void* d_x,
                            int64_t x_rows, int32_t activation, void* d_y, void* stream);
+
+/* y = act((x W^T) * x_scale * w_scale) in 8-bit integers, for num_rows rows and
+ * one matrix (EP_WEIGHT_INT8, num_experts == 1):
+ *   d_x int8 [num_rows, cols], 16-byte aligned, and d_x_scales fp32 [num_rows]: a
+ *   dispatch's codes and scales with EP_QUANT_INT8 and quant_group = hidden, or
+ *   ep_quantize_rows'; all 256 codes are values.  d_y bf16 [num_rows, M] (or
+ *   [num_rows, M/2] with EP_ACT_SWIGLU), not overlapping x.
+ *   Sums are exact; a sum, rounded to fp32, is multiplied by its row's scale, then
+ *   by its output's, in fp32, and after the activation rounded to bf16 once.
+ *   num_rows * M below 2^35. */
+ep_status ep_matmul(const ep_weights* w, const void* d_x, const float* d_x_scales,
+                    int64_t num_rows, int32_t activation, void* d_y, void* stream);
+
+/* The same for received rows, each with its expert's matrix: rows, layout, flags
+ * and states as ep_expert_matvec; the scales of rows that hold no token are not
+ * read either. */
+ep_status ep_expert_matmul(const ep_handle* h, const ep_weights* w, const void* d_x,
+                           const float* d_x_scales, int64_t x_rows, int32_t activation, void* d_y,
+                           void* stream);
 
 /* Bytes of device workspace that ep_moe_layer needs for num_tokens tokens. */
 ep_status ep_moe_workspace_size(const ep_handle* h, const ep_weights* w_up,
