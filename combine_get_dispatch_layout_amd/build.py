@@ -21,7 +21,7 @@ ARCH = "gfx950"
 SOURCES = ["layout.hip", "dispatch.hip", "fused.hip", "sources.hip", "nonexpand.hip",
            "combine.hip", "overlap.hip", "api.cpp", "gate.hip", "balance.hip", "experts.hip", "experts_bf16.hip",
            "experts_mxfp4.hip", "experts_int4_g32.hip", "experts_int4_g64.hip",
-           "experts_int4_g128.hip", "experts_int8.hip", "moe_api.cpp"]
+           "experts_int4_g128.hip", "experts_int8.hip", "matmul.hip", "moe_api.cpp"]
 PROBE_SOURCES = ["probe.hip"]
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 instructions.

@@ -9,7 +9,6 @@ hipError_t launch_product_mxfp4(const ProductArgs& a, int epilogue, hipStream_t 
 hipError_t launch_product_int4_g32(const ProductArgs& a, int epilogue, hipStream_t s);
 hipError_t launch_product_int4_g64(const ProductArgs& a, int epilogue, hipStream_t s);
 hipError_t launch_product_int4_g128(const ProductArgs& a, int epilogue, hipStream_t s);
-hipError_t launch_product_int8(const ProductArgs& a, int epilogue, hipStream_t s);
 
 hipError_t launch_down_few_bf16(const ProductArgs& a, bool* done, hipStream_t s);
 hipError_t launch_down_few_mxfp4(const ProductArgs& a, bool* done, hipStream_t s);
@@ -35,7 +34,6 @@ hipError_t launch_product(ProductArgs a, int epilogue, hipStream_t s)
         case kMxfp4: return launch_product_mxfp4(a, epilogue, s);
         case kInt4G32: return launch_product_int4_g32(a, epilogue, s);
         case kInt4G64: return launch_product_int4_g64(a, epilogue, s);
-        case kInt8: return launch_product_int8(a, epilogue, s);
         default: return launch_product_int4_g128(a, epilogue, s);
     }
 }

@@ -91,6 +91,8 @@ hipError_t launch_product(ProductArgs a, int epilogue, hipStream_t s);
 // The same as kStoreF32 and launch_layer_reduce in one kernel, y = bf16 [N, H],
 // where the batch is small enough for it (*done).
 hipError_t launch_down_few(const ProductArgs& a, bool* done, hipStream_t s);
+// Products in 8-bit integers (kInt8): y = bf16, gated or not.
+hipError_t launch_matmul(const ProductArgs& a, bool gate, hipStream_t s);
 hipError_t launch_layer_reduce(const ReduceArgs& a, hipStream_t s);
 hipError_t launch_gate(const GateArgs& a, hipStream_t s);
 hipError_t launch_gate_backward(const GateArgs& a, hipStream_t s);

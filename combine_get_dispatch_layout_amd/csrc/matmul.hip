@@ -1,0 +1,449 @@
+// Products of many int8 rows with int8 weights on gfx950: a tiled kernel on the
+// matrix cores.
+//
+// What is computed, for a tile of BM rows of one expert and BN of its weight
+// rows: sum[m][n] = sum over k of W[n][k] x[m][k], exact in 32-bit integers, by
+// v_mfma_i32_16x16x64_i8 with the weight rows as A and the rows of x as B, so
+// that a lane's sums are four neighbouring outputs of one row of x; then scales,
+// activation, one rounding.
+//
+// Both operands go from memory straight to LDS (buffer loads with an LDS
+// destination), S stages of 128 columns in a ring, and from there to registers.
+//  - 128 columns: a row's share of a load is a whole cache line.  With 64 columns
+//    and twice the stages, the same bytes take twice the requests: 4096 rows,
+//    7168 -> 4096, 118 us, with 128 columns 108 us.
+//  - A load puts lane l's 16 bytes at 16 l, so the order of a row's eight pieces
+//    in LDS is chosen by which piece a lane asks for: piece j of row r lies at
+//    j ^ (r % 8), and the eight lanes that LDS serves at a time (eight rows, one
+//    piece) find eight different places.  No bank conflicts are counted.
+//  - Lanes whose row or columns are past the end ask for an address outside the
+//    buffer: they get zeros and cost no traffic.
+// Blocks stay: each takes tile after tile, and the loads run S - 1 stages ahead
+// of the arithmetic across tile borders, so a new tile starts with its columns
+// there.  Scales of a tile's rows and outputs ride along with its first stage.
+//
+// An expert's rows are spread evenly over its tiles, in 16s, and a tile's
+// arithmetic skips groups of 16 rows behind the last.  Tiles are numbered so that
+// the blocks of an XCD (blockIdx % 8), which share an L2, work side by side: a
+// contiguous share of all tiles each, four tiles of rows by the tiles of outputs.
+//
+// What bounds it: power, and behind that the way through LDS.  4096 rows, 7168 ->
+// 4096 run at 1.8 GHz of 2.4.
+#include "experts.hpp"
+#include "matmul_shape.hpp"
+
+namespace epk {
+
+hipError_t launch_product_int8(const ProductArgs& a, int epilogue, hipStream_t s);
+
+namespace mm {
+namespace {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+struct Args {
+    const uint8_t* w;           // [E, rows, cols]
+    const float* w_scales;      // [E, rows]
+    int rows, cols, units;
+    bool vec;                   // rows of y take vectors of eight
+    const uint8_t* x;           // [.., cols]
+    const float* x_scales;
+    int64_t num_rows;
+    int E;
+    const int32_t* psum;        // of received rows, else null
+    const int32_t* count;
+    int cap;
+    uint16_t* y;                // [.., units]
+    uint32_t* flags;
+};
+
+typedef __amdgpu_buffer_rsrc_t Buffer;
+
+__device__ __forceinline__ Buffer make_buffer(const void* base, int64_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+}
+
+// 16 bytes a lane from memory straight to LDS, lane after lane.
+__device__ __forceinline__ void load_to_lds(Buffer b, unsigned char* to, uint32_t lane_off, uint32_t off)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 16, lane_off, off, 0, 0);
+}
+
+// 4 bytes a lane.
+__device__ __forceinline__ void load_word_to_lds(Buffer b, unsigned char* to, uint32_t lane_off)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 4, lane_off, 0, 0, 0);
+}
+
+constexpr uint32_t kNowhere = 0x80000000u;      // past every buffer: reads 0
+
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+// BM rows of x and BN weight rows, shared by WM x WN waves.
+template <int BM, int BN, int WM, int WN, int S, bool GATE>
+struct Tile {
+    static constexpr int kWaves = WM * WN, kThreads = kWave * kWaves;
+    static constexpr int kLoadRows = 1024 / kStep;              // of a load
+    static constexpr int kXLoads = BM / kLoadRows / kWaves, kWLoads = BN / kLoadRows / kWaves;
+    static constexpr int kLoads = kXLoads + kWLoads;            // of a wave a stage
+    static constexpr int MT = BM / 16 / WM, NT = BN / 16 / WN;  // groups of 16 of a wave
+    static constexpr int kStageBytes = (BM + BN) * kStep;
+    static constexpr int kUnits = GATE ? BN / 2 : BN;
+    static constexpr int kScaleBytes = (BM + BN) * 4, kScaleLoads = (BM + BN) / 64;
+    static constexpr int kLds = S * kStageBytes + 2 * kScaleBytes;
+    // blocks of a CU: 160 KB of LDS, 5 KB of which are static
+    static constexpr int kBlocks = 163840 / (kLds + 5632);
+    static_assert(BM % (kLoadRows * kWaves) == 0 && BN % (kLoadRows * kWaves) == 0, "whole loads");
+    static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && BM % 64 == 0 && BN % 64 == 0, "whole groups");
+    // gate and up groups alternate; a wave's loads are of one kind
+    static_assert(!GATE || (NT % 2 == 0 && kWaves * kLoadRows % 32 == 0), "pairs of groups");
+};
+
+// A tile of one expert.
+struct Where {
+    int expert, rows;
+    int64_t row0;
+    int unit0;
+};
+
+template <int BM, int BN, int WM, int WN, int S, bool GATE>
+__global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S, GATE>::kBlocks)) void k_matmul(Args a)
+{
+    using T = Tile<BM, BN, WM, WN, S, GATE>;
+    constexpr int MT = T::MT, NT = T::NT;
+    extern __shared__ __align__(1024) unsigned char smem[];     // stages, scales of two tiles
+    __shared__ int tile0[kMaxExperts + 1];      // tiles of rows before each expert
+    __shared__ int wave_sum[T::kWaves];
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave % WM, wn = wave / WM;
+    const int n = lane & 15, c = lane >> 4;
+    const bool grouped = a.count != nullptr;
+
+    // ---- which tiles there are
+    auto rows_of = [&](int e, int64_t* row0, bool flag) -> int64_t {
+        if (!grouped) {
+            *row0 = 0;
+            return a.num_rows;
+        }
+        int64_t r = a.count[e];
+        *row0 = a.psum[e];
+        if (a.cap > 0 && r > a.cap) r = a.cap;
+        if (*row0 + r > a.num_rows) {
+            r = *row0 < a.num_rows ? a.num_rows - *row0 : 0;
+            if (flag && blockIdx.x == 0) atomicOr(a.flags, kFlagCapacity);
+        }
+        return r;
+    };
+    int tiles_m = 0;
+    if (grouped) {
+        for (int e0 = 0; e0 < a.E; e0 += T::kThreads) {
+            const int e = e0 + tid;
+            int64_t row0;
+            const int t = e < a.E ? (int)((rows_of(e, &row0, true) + BM - 1) / BM) : 0;
+            int upto = t;
+#pragma unroll
+            for (int d = 1; d < kWave; d *= 2) {
+                const int v = __shfl_up(upto, d);
+                if (lane >= d) upto += v;
+            }
+            if (lane == kWave - 1) wave_sum[wave] = upto;
+            __syncthreads();
+            int before = tiles_m;
+            for (int w = 0; w < T::kWaves; ++w) {
+                if (w < wave) before += wave_sum[w];
+                tiles_m += wave_sum[w];
+            }
+            if (e < a.E) tile0[e] = before + upto - t;
+            __syncthreads();
+        }
+        if (tid == 0) tile0[a.E] = tiles_m;
+        __syncthreads();
+        tiles_m = __builtin_amdgcn_readfirstlane(tiles_m);
+    } else {
+        tiles_m = (int)((a.num_rows + BM - 1) / BM);
+    }
+    const uint32_t tiles_n = (uint32_t)((a.units + T::kUnits - 1) / T::kUnits);
+    const uint32_t total = (uint32_t)tiles_m * tiles_n;         // below 2^32: rows * outputs are below 2^35
+    const uint32_t xcd = blockIdx.x % 8, stride = gridDim.x / 8;
+    const uint32_t share = total / 8, more = total % 8;
+    uint32_t at = xcd * share + min(xcd, more);
+    const uint32_t stop = at + share + (xcd < more ? 1u : 0u);
+    at += blockIdx.x / 8;
+    if (at >= stop) return;
+
+    auto locate = [&](uint32_t t, Where& o) {
+        int e = 0, first = 0, mt = tiles_m;
+        if (grouped) {
+            // the last expert whose tiles start at or before t, in two probes
+            const int per = (a.E + kWave - 1) / kWave;
+            auto starts = [&](int i) { return i < a.E && (uint32_t)tile0[min(i, a.E)] * tiles_n <= t; };
+            const int g = (63 - (int)__builtin_clzll(__ballot(starts(lane * per)))) * per;
+            e = g + 63 - (int)__builtin_clzll(__ballot(lane < per && starts(g + lane)));
+            e = __builtin_amdgcn_readfirstlane(e);
+            first = __builtin_amdgcn_readfirstlane(tile0[e]);
+            mt = __builtin_amdgcn_readfirstlane(tile0[e + 1]) - first;
+        }
+        const uint32_t i = t - (uint32_t)first * tiles_n;
+        constexpr uint32_t kSide = 4;
+        const uint32_t band = i / (kSide * tiles_n), r = i - band * kSide * tiles_n;
+        const uint32_t side = min(kSide, (uint32_t)mt - band * kSide);
+        const uint32_t m = band * kSide + r % side;
+        int64_t row0;
+        const int64_t rows = rows_of(e, &row0, false), each = ((rows + 15) / 16 + mt - 1) / mt * 16;
+        const int64_t from = row0 + m * each, left = rows - m * each;
+        o.expert = e;
+        o.unit0 = (int)(r / side) * T::kUnits;
+        o.rows = __builtin_amdgcn_readfirstlane((int)(left < each ? left : each));
+        o.row0 = (int64_t)__builtin_amdgcn_readfirstlane((int)(from >> 32)) << 32 |
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)from);
+    };
+
+    const int steps = (a.cols + kStep - 1) / kStep;
+
+    // ---- loads, S - 1 stages ahead of the arithmetic
+    const int l_row = lane / 8, l_piece = lane % 8 ^ l_row;
+    const bool l_up = GATE && wave * T::kLoadRows / 16 % 2;     // this wave loads up rows
+    const int last_cols = a.cols - (steps - 1) * kStep;         // of the last step
+    uint32_t xo[T::kXLoads], wo[T::kWLoads];
+    Buffer xb, wb;
+    int l_step = 0, l_parity = 0;
+    uint32_t l_tile = at;
+    unsigned char* const scales = smem + S * T::kStageBytes;
+    auto aim = [&] {
+        Where p;
+        locate(l_tile, p);
+        xb = make_buffer(a.x + p.row0 * a.cols, (int64_t)p.rows * a.cols);
+#pragma unroll
+        for (int j = 0; j < T::kXLoads; ++j) {
+            const int r = (j * T::kWaves + wave) * T::kLoadRows + l_row;
+            xo[j] = r < p.rows ? (uint32_t)r * (uint32_t)a.cols + 16u * l_piece : kNowhere;
+        }
+        const int have = min(T::kUnits, a.units - p.unit0);
+        const int64_t w0 = (int64_t)p.expert * a.rows + (l_up ? a.units : 0) + p.unit0;
+        wb = make_buffer(a.w + w0 * a.cols, (int64_t)have * a.cols);
+#pragma unroll
+        for (int j = 0; j < T::kWLoads; ++j) {
+            const int r = (j * T::kWaves + wave) * T::kLoadRows + l_row;
+            const int u = GATE ? r / 32 * 16 + r % 16 : r;
+            wo[j] = u < have ? (uint32_t)u * (uint32_t)a.cols + 16u * l_piece : kNowhere;
+        }
+        // scales of its rows, then of its outputs in the order of the groups
+        const Buffer xs = make_buffer(a.x_scales + p.row0, 4 * (int64_t)p.rows);
+        const Buffer ws = make_buffer(a.w_scales + (int64_t)p.expert * a.rows, 4 * (int64_t)a.rows);
+        for (int q = wave; q < T::kScaleLoads; q += T::kWaves) {
+            unsigned char* const to = scales + l_parity * T::kScaleBytes + q * 256;
+            if (q < BM / 64) {
+                load_word_to_lds(xs, to, (uint32_t)(q * 64 + lane) * 4);
+            } else {
+                const int r = (q - BM / 64) * 64 + lane;
+                const int u = p.unit0 + (GATE ? r / 32 * 16 + r % 16 : r);
+                load_word_to_lds(ws, to, u < a.units ? (uint32_t)(u + (GATE && r / 16 % 2 ? a.units : 0)) * 4 : kNowhere);
+            }
+        }
+        l_parity ^= 1;
+    };
+    auto load_stage = [&](int buf) {
+        if (l_tile >= stop) return;
+        unsigned char* const to = smem + buf * T::kStageBytes + wave * 1024;
+        const uint32_t k0 = (uint32_t)l_step * kStep;
+        const bool past = l_step == steps - 1 && 16 * l_piece >= last_cols;
+#pragma unroll
+        for (int j = 0; j < T::kXLoads; ++j)
+            load_to_lds(xb, to + j * T::kWaves * 1024, past ? kNowhere : xo[j], k0);
+#pragma unroll
+        for (int j = 0; j < T::kWLoads; ++j)
+            load_to_lds(wb, to + BM * kStep + j * T::kWaves * 1024, past ? kNowhere : wo[j], k0);
+        if (++l_step == steps) {
+            l_step = 0;
+            l_tile += stride;
+            if (l_tile < stop) aim();
+        }
+    };
+
+    // operands of half h of a step: 16 rows, the lane's 16 of 64 columns
+    const int frag = n * kStep, piece = c ^ (n & 7);
+    auto operand = [&](int buf, int row, int h) {
+        return *reinterpret_cast<const i32x4*>(smem + buf * T::kStageBytes + row * kStep + frag + (piece ^ 4 * h) * 16);
+    };
+
+    aim();
+#pragma unroll 1
+    for (int s = 0; s < S - 1; ++s) load_stage(s);
+    Where p;
+    locate(at, p);
+    int live = (p.rows + 15) / 16, parity = 0;      // groups of rows; scales
+    i32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    int step = 0, buf = 0;
+    for (;;) {
+        // this step's columns have arrived, and at the barrier for every wave;
+        // the stage that is loaded next has been read.  (Behind the last load
+        // nothing newer is on its way.)
+        if (l_tile < stop) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 2) * T::kLoads) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        load_stage(buf == 0 ? S - 1 : buf - 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            i32x4 xf[MT], wf[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) wf[j] = operand(buf, BM + (wn * NT + j) * 16, h);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) xf[i] = operand(buf, (i * WM + wm) * 16, h);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                if (__builtin_expect(i * WM + wm < live, 1)) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[j], xf[i], acc[i][j], 0, 0, 0);
+                }
+        }
+        buf = buf == S - 1 ? 0 : buf + 1;
+        if (++step < steps) continue;
+        step = 0;
+
+        // ---- store: this lane has outputs 4c .. 4c+3 of row n of each group
+        constexpr int NO = GATE ? NT / 2 : NT;      // groups of outputs
+        const float* const xs = reinterpret_cast<const float*>(scales + parity * T::kScaleBytes) + n;
+        const f32x4* const ws =
+            reinterpret_cast<const f32x4*>(scales + parity * T::kScaleBytes + 4 * BM) + wn * NT * 4 + c;
+        f32x4 w4[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) w4[j] = ws[j * 4];
+        const int u0 = p.unit0 + wn * NO * 16;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int m = (i * WM + wm) * 16 + n;
+            if ((i * WM + wm) * 16 >= p.rows) continue;
+            const float x1 = xs[(i * WM + wm) * 16];
+            uint32_t lo[NO], hi[NO];
+#pragma unroll
+            for (int o = 0; o < NO; ++o) {
+                float v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[q] = (float)acc[i][GATE ? 2 * o : o][q] * x1 * w4[GATE ? 2 * o : o][q];
+                    // (the exponential is good to 2^-24 of its argument)
+                    if constexpr (GATE)
+                        v[q] = v[q] / (1.f + __expf(-v[q])) * ((float)acc[i][2 * o + 1][q] * x1 * w4[2 * o + 1][q]);
+                }
+                const u32x2 d = __builtin_bit_cast(u32x2, __builtin_convertvector(f32x4{v[0], v[1], v[2], v[3]}, bf16x4));
+                lo[o] = d[0];
+                hi[o] = d[1];
+            }
+            uint16_t* const to = a.y + (p.row0 + m) * a.units;
+            if (a.vec) {
+                // two groups: their lanes trade, 8 outputs of one group each
+#pragma unroll
+                for (int o = 0; o + 1 < NO; o += 2) {
+                    swap16(lo[o], lo[o + 1]);
+                    swap16(hi[o], hi[o + 1]);
+                    const int u = u0 + (o + c % 2) * 16 + c / 2 * 8;
+                    if (m < p.rows && u < a.units)
+                        *reinterpret_cast<u32x4*>(to + u) = u32x4{lo[o], hi[o], lo[o + 1], hi[o + 1]};
+                }
+                if constexpr (NO % 2 != 0) {
+                    const int u = u0 + (NO - 1) * 16 + 4 * c;
+                    if (m < p.rows && u < a.units) *reinterpret_cast<u32x2*>(to + u) = u32x2{lo[NO - 1], hi[NO - 1]};
+                }
+            } else if (m < p.rows) {
+#pragma unroll
+                for (int o = 0; o < NO; ++o)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int u = u0 + o * 16 + 4 * c + q;
+                        if (u < a.units) to[u] = (uint16_t)((q < 2 ? lo[o] : hi[o]) >> (q % 2 * 16));
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+        at += stride;
+        if (at >= stop) return;
+        parity ^= 1;
+        locate(at, p);
+        live = (p.rows + 15) / 16;
+    }
+}
+
+int num_cus()
+{
+    static const int n = [] {
+        int dev = 0, v = 0;
+        if (hipGetDevice(&dev) != hipSuccess ||
+            hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v < 8)
+            v = 256;
+        return v;
+    }();
+    return n;
+}
+
+template <int BM, int BN, int WM, int WN, int S, bool GATE>
+hipError_t launch_tile(const Args& a, int64_t rows, hipStream_t s)
+{
+    using T = Tile<BM, BN, WM, WN, S, GATE>;
+    // every expert may end in a tile of its own
+    const int64_t tiles = ((rows + BM - 1) / BM + (a.count ? a.E : 0)) * ((a.units + T::kUnits - 1) / T::kUnits);
+    const int64_t most = (int64_t)num_cus() / 8 * T::kBlocks, need = (tiles + 7) / 8;
+    const dim3 grid((unsigned)(8 * (need < most ? need : most)));
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_matmul<BM, BN, WM, WN, S, GATE>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+    hipLaunchKernelGGL((k_matmul<BM, BN, WM, WN, S, GATE>), grid, dim3(T::kThreads), (size_t)T::kLds, s, a);
+    return hipGetLastError();
+}
+
+template <bool GATE>
+hipError_t launch_path(Path path, const Args& a, int64_t rows, hipStream_t s)
+{
+    switch (path) {
+        case kPathTile64: return launch_tile<64, 128, 1, 4, stages(kPathTile64), GATE>(a, rows, s);
+        case kPathTile128: return launch_tile<128, 128, 2, 2, stages(kPathTile128), GATE>(a, rows, s);
+        default: return launch_tile<256, 256, 2, 4, stages(kPathTile256), GATE>(a, rows, s);
+    }
+}
+
+}  // namespace
+}  // namespace mm
+
+hipError_t launch_matmul(const ProductArgs& p, bool gate, hipStream_t s)
+{
+    const int64_t rows = p.count ? p.P : p.num_rows, cols = 2 * (int64_t)p.w.cols;
+    const mm::Path path = mm::choose_path(gate, cols, p.units, p.count ? p.E : 1, rows);
+    if (path == mm::kPathNone) return hipSuccess;
+    if (path == mm::kPathFew) return launch_product_int8(p, gate ? kSwigluBf16 : kStoreBf16, s);
+    mm::Args a = {};
+    a.w = p.w.data;
+    a.w_scales = reinterpret_cast<const float*>(p.w.scales);
+    a.rows = p.w.rows;
+    a.cols = (int)cols;
+    a.units = p.units;
+    a.vec = p.units % 8 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
+    a.x = reinterpret_cast<const uint8_t*>(p.x);
+    a.x_scales = p.x_scales;
+    a.num_rows = p.num_rows;
+    a.E = p.E;
+    a.psum = p.psum;
+    a.count = p.count;
+    a.cap = p.cap;
+    a.y = static_cast<uint16_t*>(p.y);
+    a.flags = p.flags;
+    return gate ? mm::launch_path<true>(path, a, rows, s) : mm::launch_path<false>(path, a, rows, s);
+}
+
+}  // namespace epk

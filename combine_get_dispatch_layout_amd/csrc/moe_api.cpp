@@ -482,8 +482,7 @@ ep_status ep_matmul(const ep_weights* w, const void* d_x, const float* d_x_scale
     if (st == EP_OK) st = check_x_scales(d_x_scales, num_rows);
     if (st != EP_OK) return st;
     a.x_scales = d_x_scales;
-    EP_HIP(epk::launch_product(a, activation == EP_ACT_SWIGLU ? epk::kSwigluBf16 : epk::kStoreBf16,
-                               static_cast<hipStream_t>(stream)));
+    EP_HIP(epk::launch_matmul(a, activation == EP_ACT_SWIGLU, static_cast<hipStream_t>(stream)));
     return EP_OK;
 }
 
@@ -496,8 +495,7 @@ ep_status ep_expert_matmul(const ep_handle* h, const ep_weights* w, const void* 
     if (st == EP_OK) st = check_x_scales(d_x_scales, x_rows);
     if (st != EP_OK) return st;
     a.x_scales = d_x_scales;
-    EP_HIP(epk::launch_product(a, activation == EP_ACT_SWIGLU ? epk::kSwigluBf16 : epk::kStoreBf16,
-                               static_cast<hipStream_t>(stream)));
+    EP_HIP(epk::launch_matmul(a, activation == EP_ACT_SWIGLU, static_cast<hipStream_t>(stream)));
     return EP_OK;
 }
 

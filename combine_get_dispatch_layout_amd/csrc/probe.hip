@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "ep_moe.h"
+#include "matmul_shape.hpp"
 #include "product_shape.hpp"
 
 namespace {
@@ -227,4 +228,9 @@ extern "C" int ep_probe_product_path(int format, int group, int gate, int terms,
 extern "C" int ep_probe_layer_in_two(int format, int group, int64_t tokens, int64_t topk, int64_t inter)
 {
     return epk::prod::few_fits(weight_kind(format, group), tokens, tokens * topk, inter) ? 1 : 0;
+}
+
+extern "C" int ep_probe_matmul_path(int gate, int64_t cols, int64_t units, int64_t experts, int64_t rows)
+{
+    return epk::mm::choose_path(gate != 0, cols, units, experts, rows);
 }
