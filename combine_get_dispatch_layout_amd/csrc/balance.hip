@@ -28,22 +28,26 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 
+// Waves of a block of the second kernel, at most.
+constexpr int kFinishWaves = 16;
+
 // A chunk: at least 16 tokens (four waves of four), so many that some 1024
 // blocks make the batch, at most 1024 (which bounds the fp32 sums' length).
 constexpr int kMinChunk = 16, kMaxChunk = 1024, kChunks = 1024;
 
+// A batch that one block takes.
+constexpr int kSmallWaves = 16, kSmallExperts = 256, kSmallTokens = 256, kSmallSequences = 4;
+
 constexpr float kLow = -__builtin_huge_valf();
 
-// exp(x) for x <= 0, off by an ulp or two: the rounding of x log2(e), which
+// exp(x) for |x| <= 150, off by an ulp or two: the rounding of x log2(e), which
 // the hardware's exp2 would magnify, is put right to first order.
-__device__ __forceinline__ float exp_neg(float x)
+__device__ __forceinline__ float exp_near(float x)
 {
-    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;      // log2(e)
-    x = fmaxf(x, -200.f);
-    const float y = x * kHi;
-    const float rest = fmaf(x, kLo, fmaf(x, kHi, -y));
+    constexpr float kLog2E = 1.44269502f;
+    const float y = x * kLog2E;
     const float r = __builtin_amdgcn_exp2f(y);
-    return fmaf(r, rest * 0.693147181f, r);
+    return fmaf(r, fmaf(x, kLog2E, -y) * 0.693147181f, r);
 }
 
 __device__ __forceinline__ float reciprocal(float d)
@@ -51,6 +55,10 @@ __device__ __forceinline__ float reciprocal(float d)
     const float r = __builtin_amdgcn_rcpf(d);
     return fmaf(fmaf(-d, r, 1.f), r, r);
 }
+
+// Below this a sigmoid is taken for 0 (it would be less than the smallest
+// normal fp32, as softmax scores below that are).
+constexpr float kFar = -87.25f;
 
 template <int LANES>
 __device__ __forceinline__ float lanes_max(float v)
@@ -72,88 +80,111 @@ __device__ __forceinline__ float lanes_sum(float v)
     return v + dpp<0x140>(v);
 }
 
+// How logits lie in memory: rows of vectors of four (E % 4 == 0, aligned), or
+// anything.
+enum Form { kVecF32, kVecBf16, kAny };
+
 // How a token's experts lie in LANES lanes: vector v of lane l holds the four
 // experts from 4 (v LANES + l) on.
-template <int LANES, int VECS>
+template <int LANES, int VECS, int FORM>
 struct Experts {
     static constexpr int kEach = 4 * VECS;           // of a lane
     static constexpr int kTokens = kWave / LANES;    // of a wave at a time
     static constexpr int kMost = LANES * kEach;
 
+    // Logits as they are loaded, to be in flight while others are worked on: no
+    // branch and no conversion stands between the loads.
+    static constexpr int kWords = FORM == kVecBf16 ? 2 : 4;
+    struct Raw {
+        uint32_t w[VECS][kWords];
+    };
+
     static __device__ __forceinline__ int first(int lane, int v) { return 4 * (v * LANES + lane % LANES); }
 
-    // Logits of token t as they are; -infinity past the last expert.
-    static __device__ __forceinline__ void load(const BalanceArgs& a, int64_t t, float (&z)[kEach])
+    static __device__ __forceinline__ void load(const BalanceArgs& a, int64_t t, Raw& o)
     {
         const int lane = threadIdx.x & (kWave - 1);
 #pragma unroll
         for (int v = 0; v < VECS; ++v) {
             const int e = first(lane, v);
-            const int64_t at = t * a.E + e;
+            const int64_t at = t * a.E + (e < a.E ? e : 0);
+            if constexpr (FORM == kVecF32) {
+                const u32x4 d = *reinterpret_cast<const u32x4*>(static_cast<const float*>(a.logits) + at);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) z[4 * v + j] = kLow;
-            if (a.vec) {        // E % 4 == 0: whole or not at all
-                if (e >= a.E) continue;
-                if (a.bf16) {
-                    const u32x2 d = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.logits) + at);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        z[4 * v + j] = __uint_as_float(j % 2 ? d[j / 2] & 0xFFFF0000u : d[j / 2] << 16);
-                } else {
-                    const f32x4 d = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.logits) + at);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) z[4 * v + j] = d[j];
-                }
+                for (int j = 0; j < 4; ++j) o.w[v][j] = d[j];
+            } else if constexpr (FORM == kVecBf16) {
+                const u32x2 d = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.logits) + at);
+                o.w[v][0] = d[0];
+                o.w[v][1] = d[1];
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (e + j < a.E) z[4 * v + j] = load_logit(a.logits, a.bf16, at + j);
+                    o.w[v][j] = __float_as_uint(load_logit(a.logits, a.bf16, t * a.E + (e + j < a.E ? e + j : 0)));
             }
         }
     }
 
-    // Logits to scores; of a sigmoid also 1 - s where GRAD asks for it.
-    template <bool GRAD>
-    static __device__ __forceinline__ void scores(const BalanceArgs& a, float (&z)[kEach], float (&rest)[GRAD ? kEach : 1])
+    // -infinity past the last expert
+    static __device__ __forceinline__ void unpack(const BalanceArgs& a, const Raw& r, float (&z)[kEach])
     {
-        float top = kLow;
+        const int lane = threadIdx.x & (kWave - 1);
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) z[i] = clean_logit(z[i]);
+        for (int i = 0; i < kEach; ++i) {
+            const int v = i / 4, j = i % 4;
+            if constexpr (FORM == kVecBf16)
+                z[i] = __uint_as_float(j % 2 ? r.w[v][j / 2] & 0xFFFF0000u : r.w[v][j / 2] << 16);
+            else
+                z[i] = __uint_as_float(r.w[v][j]);
+        }
+        if (a.E < kMost)
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                z[i] = first(lane, i / 4) + (FORM == kAny ? i % 4 : 0) < a.E ? z[i] : kLow;
+    }
+
+    // Logits to scores, up to the returned factor; of a sigmoid also 1 - s where
+    // GRAD asks for it.
+    template <bool GRAD>
+    static __device__ __forceinline__ float scores(const BalanceArgs& a, float (&z)[kEach], float (&rest)[GRAD ? kEach : 1])
+    {
+        // (maxima pass over NaN, comparisons with it are false)
         const bool divide = a.scoring == 0 || a.normalize;
+        float top = kLow;
         if (divide) {
 #pragma unroll
             for (int i = 0; i < kEach; ++i) top = fmaxf(top, z[i]);
             top = lanes_max<LANES>(top);
         }
-        float total = 0.f;
-        if (a.scoring == 0) {
+        constexpr float kHighest = 3.402823466e38f;
+        if (a.scoring == 0 && top > kHighest) {     // +infinity: the largest float
+            top = kHighest;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) z[i] = z[i] > kHighest ? kHighest : z[i];
+        }
+        // normalised sigmoids that have all but run out of range go in
+        // proportion to their exponentials, as a softmax's (1 - s is 1 there)
+        if (a.scoring == 0 || (divide && top < -64.f)) {
+            // (a NaN, also -infinity less itself, becomes the least there is)
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                z[i] = z[i] > kLow ? exp_neg(z[i] - top) : 0.f;
-                total += z[i];
+                z[i] = exp_near(fmaxf(z[i] - top, -150.f));
+                if constexpr (GRAD) rest[i] = 1.f;
             }
         } else {
-            // normalised sigmoids that have all but run out of range go in
-            // proportion to their exponentials, from the largest one down
-            const bool far = divide && top < -64.f;
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                const bool in = z[i] > kLow;
-                const float x = exp_neg(-fabsf(z[i]));
-                const float r = reciprocal(1.f + x);
-                if constexpr (GRAD) rest[i] = z[i] >= 0.f ? x * r : r;
-                float s = z[i] >= 0.f ? r : x * r;
-                if (far) s = exp_neg(z[i] - top);
-                z[i] = in ? s : 0.f;
-                total += z[i];
+                const float x = exp_near(-__builtin_amdgcn_fmed3f(z[i], kFar, 150.f));
+                const float r = __builtin_amdgcn_rcpf(1.f + x);
+                if constexpr (GRAD) rest[i] = x * r;
+                z[i] = z[i] > kFar ? r : 0.f;
             }
         }
-        if (divide) {
-            total = lanes_sum<LANES>(total);
-            const float inv = total > 0.f ? reciprocal(total) : 0.f;
+        if (!divide) return 1.f;
+        float total = 0.f;
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) z[i] *= inv;
-        }
+        for (int i = 0; i < kEach; ++i) total += z[i];
+        total = lanes_sum<LANES>(total);
+        return total > 0.f ? reciprocal(total) : 0.f;
     }
 };
 
@@ -184,16 +215,70 @@ __device__ __forceinline__ int first_sequence(const BalanceArgs& a, int64_t t)
     return lo;
 }
 
-// Adds up each piece of the block's chunk: scores, entries, tokens.
-template <int LANES, int VECS>
-__global__ __launch_bounds__(kThreads) void k_balance_pieces(BalanceArgs a)
+// What the tokens [t0, t1) add up to, by the block's W waves, in LDS.
+template <typename X, int W>
+struct Piece {
+    float sums[W][X::kMost];    // of scores, a wave's share
+    int counts[X::kMost];
+    int tokens[W];              // unmasked ones, a wave's share
+};
+
+// Ends at a barrier; the caller places one before the next piece.
+template <typename X, int W>
+__device__ __forceinline__ void add_up(const BalanceArgs& a, int64_t t0, int64_t t1, Piece<X, W>& out)
 {
-    using X = Experts<LANES, VECS>;
-    __shared__ float sums[kWaves][X::kMost];
-    __shared__ int counts[X::kMost];
-    __shared__ int tokens[kWaves];
+    constexpr int kLanes = kWave / X::kTokens;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    for (int e = tid; e < X::kMost; e += W * kWave) out.counts[e] = 0;
+    __syncthreads();
+    const int entries = (int)(t1 - t0) * a.K;
+    for (int i = tid; i < entries; i += W * kWave) {
+        const int t = a.k_magic ? (int)__umulhi((uint32_t)i, a.k_magic) : i;
+        if (a.mask && a.mask[t0 + t] == 0) continue;
+        const int e = a.topk[t0 * a.K + i];
+        if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&out.counts[e], 1);
+    }
+
+    float acc[X::kEach], z[X::kEach], none[1];
+#pragma unroll
+    for (int i = 0; i < X::kEach; ++i) acc[i] = 0.f;
+    int live = 0;
+    typename X::Raw next;
+    const int64_t mine = t0 + wave * X::kTokens + lane / kLanes;
+    auto counted = [&](int64_t t) { return t < t1 && (!a.mask || a.mask[t] != 0); };
+    auto held = [&](int64_t t) { return t < t1 ? t : t0; };     // a token of the piece
+    bool in = counted(mine);
+    if (t0 < t1) X::load(a, held(mine), next);
+    for (int64_t t = mine; t - lane / kLanes < t1; t += W * X::kTokens) {
+        const bool now = in;
+        X::unpack(a, next, z);
+        in = counted(t + W * X::kTokens);
+        X::load(a, held(t + W * X::kTokens), next);
+        live += (int)__popcll(__ballot(now)) / kLanes;
+        const float by = X::template scores<false>(a, z, none);
+        const float all = now ? by : 0.f;
+#pragma unroll
+        for (int i = 0; i < X::kEach; ++i) acc[i] = fmaf(z[i], all, acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < X::kEach; ++i)
+#pragma unroll
+        for (int d = kLanes; d < kWave; d *= 2) acc[i] += __shfl_xor(acc[i], d);
+    if (lane < kLanes)
+#pragma unroll
+        for (int i = 0; i < X::kEach; ++i) out.sums[wave][X::first(lane, i / 4) + i % 4] = acc[i];
+    if (lane == 0) out.tokens[wave] = live;
+    __syncthreads();
+}
+
+// Adds up each piece of the block's chunk.
+template <int LANES, int VECS, int FORM>
+__global__ __launch_bounds__(kThreads) void k_balance_pieces(BalanceArgs a)
+{
+    using X = Experts<LANES, VECS, FORM>;
+    __shared__ Piece<X, kWaves> piece;
+    const int tid = threadIdx.x;
     if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
     const int64_t c0 = (int64_t)blockIdx.x * a.chunk;
     const int64_t c1 = c0 + a.chunk < a.N ? c0 + a.chunk : a.N;
@@ -203,128 +288,119 @@ __global__ __launch_bounds__(kThreads) void k_balance_pieces(BalanceArgs a)
         if (s0 >= c1) break;
         const int64_t t0 = s0 > c0 ? s0 : c0, t1 = s1 < c1 ? s1 : c1;
         if (t0 >= t1) continue;
-
-        for (int e = tid; e < X::kMost; e += kThreads) counts[e] = 0;
-        __syncthreads();
-        const int entries = (int)(t1 - t0) * a.K;
-        for (int i = tid; i < entries; i += kThreads) {
-            const int t = a.k_magic ? (int)__umulhi((uint32_t)i, a.k_magic) : i;
-            if (a.mask && a.mask[t0 + t] == 0) continue;
-            const int e = a.topk[t0 * a.K + i];
-            if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&counts[e], 1);
-        }
-
-        float acc[X::kEach], z[X::kEach], next[X::kEach], none[1];
-#pragma unroll
-        for (int i = 0; i < X::kEach; ++i) acc[i] = 0.f;
-        int live = 0;
-        const int64_t mine = t0 + wave * X::kTokens + lane / LANES;
-        auto counted = [&](int64_t t) { return t < t1 && (!a.mask || a.mask[t] != 0); };
-        bool in = counted(mine);
-        if (in) X::load(a, mine, next);
-        for (int64_t t = mine; t - lane / LANES < t1; t += kWaves * X::kTokens) {
-            const bool now = in;
-#pragma unroll
-            for (int i = 0; i < X::kEach; ++i) z[i] = next[i];
-            in = counted(t + kWaves * X::kTokens);
-            if (in) X::load(a, t + kWaves * X::kTokens, next);
-            live += (int)__popcll(__ballot(now)) / LANES;
-            if (now) {
-                X::template scores<false>(a, z, none);
-#pragma unroll
-                for (int i = 0; i < X::kEach; ++i) acc[i] += z[i];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < X::kEach; ++i)
-#pragma unroll
-            for (int d = LANES; d < kWave; d *= 2) acc[i] += __shfl_xor(acc[i], d);
-        if (lane < LANES)
-#pragma unroll
-            for (int i = 0; i < X::kEach; ++i) sums[wave][X::first(lane, i / 4) + i % 4] = acc[i];
-        if (lane == 0) tokens[wave] = live;
-        __syncthreads();
+        add_up<X, kWaves>(a, t0, t1, piece);
         const int64_t slot = (int64_t)blockIdx.x + q;
         for (int e = tid; e < a.E; e += kThreads) {
-            a.part_sum[slot * a.E + e] = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
-            a.part_count[slot * a.E + e] = counts[e];
+            a.part_sum[slot * a.E + e] = (piece.sums[0][e] + piece.sums[1][e]) + (piece.sums[2][e] + piece.sums[3][e]);
+            a.part_count[slot * a.E + e] = piece.counts[e];
         }
-        if (tid == 0) a.part_tokens[slot] = (tokens[0] + tokens[1]) + (tokens[2] + tokens[3]);
+        if (tid == 0) a.part_tokens[slot] = (piece.tokens[0] + piece.tokens[1]) + (piece.tokens[2] + piece.tokens[3]);
         __syncthreads();
     }
 }
 
-// Adds up a sequence's pieces for `slice` experts; the last block to finish
-// adds up the blocks' shares of the loss, in their order.
-__global__ __launch_bounds__(kThreads) void k_balance_finish(BalanceArgs a, int slice, int slices)
+// A small batch in one block, without the second kernel: what a call of few
+// tokens costs is its launches.  128 tokens, 16 experts: 16.5 us as issued from
+// Python in two kernels.
+template <int LANES, int VECS, int FORM>
+__global__ __launch_bounds__(kSmallWaves* kWave) void k_balance_small(BalanceArgs a)
 {
-    __shared__ double sums[kThreads];
-    __shared__ int counts[kThreads];
-    __shared__ bool last;
-    const int tid = threadIdx.x;
-    const int q = blockIdx.x / slices, e0 = (blockIdx.x % slices) * slice;
+    using X = Experts<LANES, VECS, FORM>;
+    static_assert(X::kMost <= kSmallExperts && kSmallExperts <= kSmallWaves * kWave, "an expert a thread");
+    __shared__ Piece<X, kSmallWaves> piece;
+    __shared__ double shares[kSmallWaves];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    double loss = 0.0;
+    for (int q = 0; q < a.Q; ++q) {
+        const int64_t s0 = a.start ? start_of(a, q) : 0, s1 = a.start ? start_of(a, (int64_t)q + 1) : a.N;
+        add_up<X, kSmallWaves>(a, s0, s1 > s0 ? s1 : s0, piece);
+        double dot = 0.0;
+        int live = 0;
+        for (int w = 0; w < kSmallWaves; ++w) live += piece.tokens[w];
+        if (tid < a.E) {
+            double sum = 0.0;
+            for (int w = 0; w < kSmallWaves; ++w) sum += (double)piece.sums[w][tid];
+            a.sums[(int64_t)q * a.E + tid] = (float)sum;
+            a.counts[(int64_t)q * a.E + tid] = piece.counts[tid];
+            dot = sum * (double)piece.counts[tid];
+        }
+        if (tid == 0) a.tokens[q] = live;
+        dot = wave_sum(dot);
+        if (lane == 0) shares[wave] = dot;
+        __syncthreads();
+        if (tid == 0 && live > 0) {
+            for (int w = 1; w < kSmallWaves; ++w) dot += shares[w];
+            loss += a.factor * dot / ((double)live * (double)live);
+        }
+    }
+    if (tid == 0) *a.loss = (float)loss;
+}
+
+__device__ __forceinline__ int wave_total(int v)
+{
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+// Adds up a sequence's pieces for 64 experts, one a lane, each wave every
+// `waves`-th piece; the last block to finish adds up the blocks' shares of the
+// loss, in their order.  A chain of loads and one barrier.
+__global__ __launch_bounds__(kFinishWaves* kWave) void k_balance_finish(BalanceArgs a, int slices)
+{
+    __shared__ double sums[kFinishWaves][kWave];
+    __shared__ int counts[kFinishWaves][kWave];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), waves = blockDim.x / kWave;
+    const int q = blockIdx.x / slices, e = (blockIdx.x % slices) * kWave + lane;
     const int64_t s0 = a.start ? start_of(a, q) : 0, s1 = a.start ? start_of(a, (int64_t)q + 1) : a.N;
     const int64_t first = s0 / a.chunk, pieces = s1 > s0 ? (s1 - 1) / a.chunk - first + 1 : 0;
     const int64_t slot0 = first + q;
 
     int live = 0;
-    for (int64_t i = tid; i < pieces; i += kThreads) live += a.part_tokens[slot0 + i];
-    const int e = e0 + tid % slice, at = tid / slice, step = kThreads / slice;
+    if (wave == 0)
+        for (int64_t i = lane; i < pieces; i += kWave) live += a.part_tokens[slot0 + i];
     double sum = 0.0;
     int count = 0;
     if (e < a.E)
-#pragma unroll 4
-        for (int64_t i = at; i < pieces; i += step) {
+#pragma unroll 8
+        for (int64_t i = wave; i < pieces; i += waves) {
             sum += (double)a.part_sum[(slot0 + i) * a.E + e];
             count += a.part_count[(slot0 + i) * a.E + e];
         }
-    counts[tid] = live;
+    sums[wave][lane] = sum;
+    counts[wave][lane] = count;
     __syncthreads();
-    for (int d = kThreads / 2; d > 0; d /= 2) {
-        if (tid < d) counts[tid] += counts[tid + d];
-        __syncthreads();
+    if (wave != 0) return;
+    for (int w = 1; w < waves; ++w) {
+        sum += sums[w][lane];
+        count += counts[w][lane];
     }
-    live = counts[0];
-    __syncthreads();
-    sums[tid] = sum;
-    counts[tid] = count;
-    __syncthreads();
-    for (int d = kThreads / 2; d >= slice; d /= 2) {
-        if (tid < d) {
-            sums[tid] += sums[tid + d];
-            counts[tid] += counts[tid + d];
-        }
-        __syncthreads();
+    live = wave_total(live);
+    if (e < a.E) {
+        a.sums[(int64_t)q * a.E + e] = (float)sum;
+        a.counts[(int64_t)q * a.E + e] = count;
     }
-    if (tid < slice && e < a.E) {
-        a.sums[(int64_t)q * a.E + e] = (float)sums[tid];
-        a.counts[(int64_t)q * a.E + e] = counts[tid];
-    }
-    if (tid < slice) sums[tid] = e < a.E ? sums[tid] * (double)counts[tid] : 0.0;
-    __syncthreads();
-    for (int d = slice / 2; d > 0; d /= 2) {
-        if (tid < d) sums[tid] += sums[tid + d];
-        __syncthreads();
-    }
+    if (blockIdx.x % slices == 0 && lane == 0) a.tokens[q] = live;
+    const double dot = wave_sum(sum * (double)count);
+    const double share = live > 0 ? a.factor * dot / ((double)live * (double)live) : 0.0;
     const int blocks = (int)gridDim.x;
-    if (tid == 0) {
-        if (e0 == 0) a.tokens[q] = live;
-        const double share = live > 0 ? a.factor * sums[0] / ((double)live * (double)live) : 0.0;
+    if (blocks == 1) {
+        if (lane == 0) *a.loss = (float)share;
+        return;
+    }
+    uint32_t before = 0;
+    if (lane == 0) {
         __hip_atomic_store(&a.part_loss[blockIdx.x], share, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)blocks - 1;
+        before = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
     }
-    __syncthreads();
-    if (!last) return;
+    if (__builtin_amdgcn_readfirstlane((int)before) != blocks - 1) return;
     sum = 0.0;
-    for (int i = tid; i < blocks; i += kThreads)
+    for (int i = lane; i < blocks; i += kWave)
         sum += __hip_atomic_load(&a.part_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    sums[tid] = sum;
-    __syncthreads();
-    for (int d = kThreads / 2; d > 0; d /= 2) {
-        if (tid < d) sums[tid] += sums[tid + d];
-        __syncthreads();
-    }
-    if (tid == 0) *a.loss = (float)sums[0];
+    sum = wave_sum(sum);
+    if (lane == 0) *a.loss = (float)sum;
 }
 
 // The gradient.  With f[e] = g coefficient / Q * E / (K T^2) * count[e]:
@@ -334,10 +410,10 @@ __global__ __launch_bounds__(kThreads) void k_balance_finish(BalanceArgs a, int 
 // Scores that sum to one leave a constant in f without effect: K T / E, what
 // every expert has of a balanced batch, is taken from the counts as an integer,
 // so that the differences do not drown in the counts' own size.
-template <int LANES, int VECS>
+template <int LANES, int VECS, int FORM>
 __global__ __launch_bounds__(kThreads) void k_balance_backward(BalanceArgs a)
 {
-    using X = Experts<LANES, VECS>;
+    using X = Experts<LANES, VECS, FORM>;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t c0 = (int64_t)blockIdx.x * a.chunk;
@@ -354,38 +430,47 @@ __global__ __launch_bounds__(kThreads) void k_balance_backward(BalanceArgs a)
         s1 = a.start ? (q < a.Q ? start_of(a, (int64_t)q + 1) : a.N) : a.N;
     };
     bounds();
-    for (int64_t t = c0 + wave * X::kTokens + lane / LANES; t - lane / LANES < c1; t += kWaves * X::kTokens) {
-        if (t >= c1) continue;
+    typename X::Raw next;
+    const int64_t mine = c0 + wave * X::kTokens + lane / LANES;
+    auto unmasked = [&](int64_t t) { return t < c1 && (!a.mask || a.mask[t] != 0); };
+    auto held = [&](int64_t t) { return t < c1 ? t : c0; };         // a token of the chunk
+    bool coming = unmasked(mine);
+    X::load(a, held(mine), next);
+    for (int64_t t = mine; t - lane / LANES < c1; t += kWaves * X::kTokens) {
         float z[X::kEach], rest[X::kEach];
-        const bool masked = a.mask && a.mask[t] == 0;
-        if (!masked) X::load(a, t, z);
+        const bool live = coming;
+        X::unpack(a, next, z);
+        coming = unmasked(t + kWaves * X::kTokens);
+        X::load(a, held(t + kWaves * X::kTokens), next);
+        if (t >= c1) continue;
         while (q < a.Q && s1 <= t) {
             ++q;
             bounds();
         }
-        const bool in = !masked && q < a.Q && s0 <= t;
+        const bool in = live && q < a.Q && s0 <= t;
         if (in && q != loaded) {
             loaded = q;
-            const int live = a.tokens_in[q];
-            const int even = divide ? (int)((int64_t)a.K * live / a.E) : 0;
+            const int tokens = a.tokens_in[q];
+            const int even = divide ? (int)((int64_t)a.K * tokens / a.E) : 0;
 #pragma unroll
             for (int i = 0; i < X::kEach; ++i) {
                 const int e = X::first(lane, i / 4) + i % 4;
                 f[i] = e < a.E ? (float)(a.counts_in[(int64_t)q * a.E + e] - even) : 0.f;
             }
-            scale = live > 0 ? (float)(g / ((double)live * (double)live)) : 0.f;
+            scale = tokens > 0 ? (float)(g / ((double)tokens * (double)tokens)) : 0.f;
         }
         if (in) {
-            X::template scores<true>(a, z, rest);
+            const float by = X::template scores<true>(a, z, rest);
             float dot = 0.f;
             if (divide) {
 #pragma unroll
                 for (int i = 0; i < X::kEach; ++i) dot = fmaf(z[i], f[i], dot);
-                dot = lanes_sum<LANES>(dot);
+                dot = lanes_sum<LANES>(dot) * by;
             }
+            const float all = by * scale;
 #pragma unroll
             for (int i = 0; i < X::kEach; ++i) {
-                z[i] *= (f[i] - dot) * scale;
+                z[i] *= (f[i] - dot) * all;
                 if (a.scoring != 0) z[i] *= rest[i];
             }
         } else {
@@ -397,43 +482,61 @@ __global__ __launch_bounds__(kThreads) void k_balance_backward(BalanceArgs a)
             const int e = X::first(lane, v);
             const int64_t at = t * a.E + e;
             const float* d = z + 4 * v;
-            if (a.vec) {
-                if (e >= a.E) continue;
-                if (a.bf16)
+            if constexpr (FORM == kVecF32) {
+                if (e < a.E)
+                    *reinterpret_cast<f32x4*>(static_cast<float*>(a.grad_logits) + at) = f32x4{d[0], d[1], d[2], d[3]};
+            } else if constexpr (FORM == kVecBf16) {
+                if (e < a.E)
                     *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.grad_logits) + at) =
                         u32x2{pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])};
-                else
-                    *reinterpret_cast<f32x4*>(static_cast<float*>(a.grad_logits) + at) = f32x4{d[0], d[1], d[2], d[3]};
-                continue;
-            }
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (e + j >= a.E) continue;
-                if (a.bf16) static_cast<uint16_t*>(a.grad_logits)[at + j] = (uint16_t)pack_bf16(d[j], 0.f);
-                else static_cast<float*>(a.grad_logits)[at + j] = d[j];
+                for (int j = 0; j < 4; ++j) {
+                    if (e + j >= a.E) continue;
+                    if (a.bf16) static_cast<uint16_t*>(a.grad_logits)[at + j] = (uint16_t)pack_bf16(d[j], 0.f);
+                    else static_cast<float*>(a.grad_logits)[at + j] = d[j];
+                }
             }
         }
     }
 }
 
-template <bool BACK, int LANES, int VECS>
+bool is_small(const BalanceArgs& a)
+{
+    return a.N <= kSmallTokens && a.E <= kSmallExperts && a.Q <= kSmallSequences;
+}
+
+template <bool BACK, int LANES, int VECS, int FORM>
 hipError_t launch_shape(const BalanceArgs& a, hipStream_t s)
 {
+    if constexpr (!BACK && LANES * VECS * 4 <= kSmallExperts) {
+        if (is_small(a)) {
+            hipLaunchKernelGGL((k_balance_small<LANES, VECS, FORM>), dim3(1), dim3(kSmallWaves * kWave), 0, s, a);
+            return hipGetLastError();
+        }
+    }
     const int64_t chunks = (a.N + a.chunk - 1) / a.chunk;
     const dim3 grid((unsigned)(chunks > 0 ? chunks : 1)), block(kThreads);
-    if constexpr (BACK) hipLaunchKernelGGL((k_balance_backward<LANES, VECS>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_balance_pieces<LANES, VECS>), grid, block, 0, s, a);
+    if constexpr (BACK) hipLaunchKernelGGL((k_balance_backward<LANES, VECS, FORM>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_balance_pieces<LANES, VECS, FORM>), grid, block, 0, s, a);
     return hipGetLastError();
+}
+
+template <bool BACK, int LANES, int VECS>
+hipError_t launch_form(const BalanceArgs& a, hipStream_t s)
+{
+    if (!a.vec) return launch_shape<BACK, LANES, VECS, kAny>(a, s);
+    return a.bf16 ? launch_shape<BACK, LANES, VECS, kVecBf16>(a, s) : launch_shape<BACK, LANES, VECS, kVecF32>(a, s);
 }
 
 template <bool BACK>
 hipError_t launch_any(const BalanceArgs& a, hipStream_t s)
 {
-    if (a.E <= 64) return launch_shape<BACK, 16, 1>(a, s);
-    if (a.E <= 128) return launch_shape<BACK, 16, 2>(a, s);
-    if (a.E <= 256) return launch_shape<BACK, 16, 4>(a, s);
-    if (a.E <= 512) return launch_shape<BACK, 64, 2>(a, s);
-    return launch_shape<BACK, 64, 4>(a, s);
+    if (a.E <= 64) return launch_form<BACK, 16, 1>(a, s);
+    if (a.E <= 128) return launch_form<BACK, 16, 2>(a, s);
+    if (a.E <= 256) return launch_form<BACK, 16, 4>(a, s);
+    if (a.E <= 512) return launch_form<BACK, 64, 2>(a, s);
+    return launch_form<BACK, 64, 4>(a, s);
 }
 
 int chunk_of(int64_t N)
@@ -450,9 +553,10 @@ BalanceCarve carve_balance(int64_t N, int E, int Q)
     BalanceCarve c;
     c.chunk = chunk_of(N);
     c.slots = (N + c.chunk - 1) / c.chunk + Q;
-    // few sequences: many blocks for each, so that its pieces are read at once
-    c.slice = Q <= 16 ? 16 : 64;
-    c.blocks = (int64_t)Q * ((E + c.slice - 1) / c.slice);
+    c.blocks = (int64_t)Q * ((E + kWave - 1) / kWave);
+    // as many waves as a sequence has pieces to go round, eight each
+    const int64_t waves = (c.slots / Q + 7) / 8;
+    c.waves = (int)(waves < 1 ? 1 : waves < kFinishWaves ? waves : kFinishWaves);
     c.sum = 0;
     c.count = c.sum + up(4 * c.slots * E);
     c.tokens = c.count + up(4 * c.slots * E);
@@ -465,8 +569,8 @@ BalanceCarve carve_balance(int64_t N, int E, int Q)
 hipError_t launch_balance(const BalanceArgs& a, const BalanceCarve& c, hipStream_t s)
 {
     const hipError_t e = launch_any<false>(a, s);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_balance_finish, dim3((unsigned)c.blocks), dim3(kThreads), 0, s, a, c.slice,
+    if (e != hipSuccess || is_small(a)) return e;
+    hipLaunchKernelGGL(k_balance_finish, dim3((unsigned)c.blocks), dim3(c.waves * kWave), 0, s, a,
                        (int)(c.blocks / a.Q));
     return hipGetLastError();
 }

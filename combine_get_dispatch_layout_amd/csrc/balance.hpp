@@ -41,7 +41,7 @@ struct BalanceArgs {
 struct BalanceCarve {
     int chunk;
     int64_t slots, blocks;      // blocks of the second kernel
-    int slice;                  // its experts a block
+    int waves;                  // of a block of it
     int64_t sum, count, tokens, loss, ticket, total;
 };
 BalanceCarve carve_balance(int64_t N, int E, int Q);

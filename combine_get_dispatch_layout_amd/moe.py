@@ -325,7 +325,7 @@ def ep_balance_loss(cfg: BalanceConfig, logits: torch.Tensor, topk_idx: torch.Te
 
     def output(name, given, dtype, shape):
         if given is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
+            return logits.new_empty(shape, dtype=dtype)
         _check_tensor(name, given, (dtype,), shape, dev)
         return given
 
