@@ -114,64 +114,110 @@ struct Where {
     int unit0;
 };
 
+// ---- which tiles there are ------------------------------------------------------
+
+// Tiles of rows before each expert.
+struct Tiles {
+    int before[kMaxExperts + 1];
+    int wave_sum[16];
+};
+
+// Rows of expert e, of which row0 is the first.
+__device__ __forceinline__ int64_t rows_of(const Args& a, int e, int64_t* row0, bool flag)
+{
+    if (a.count == nullptr) {
+        *row0 = 0;
+        return a.num_rows;
+    }
+    int64_t r = a.count[e];
+    *row0 = a.psum[e];
+    if (a.cap > 0 && r > a.cap) r = a.cap;
+    if (*row0 + r > a.num_rows) {
+        r = *row0 < a.num_rows ? a.num_rows - *row0 : 0;
+        if (flag && blockIdx.x == 0) atomicOr(a.flags, kFlagCapacity);
+    }
+    return r;
+}
+
+// The tiles of BM rows that all experts have together, by WAVES waves.
+template <int BM, int WAVES>
+__device__ __forceinline__ int count_tiles(const Args& a, Tiles& o)
+{
+    if (a.count == nullptr) return (int)((a.num_rows + BM - 1) / BM);
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    int all = 0;
+    for (int e0 = 0; e0 < a.E; e0 += WAVES * kWave) {
+        const int e = e0 + tid;
+        int64_t row0;
+        const int t = e < a.E ? (int)((rows_of(a, e, &row0, true) + BM - 1) / BM) : 0;
+        int upto = t;
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+            const int v = __shfl_up(upto, d);
+            if (lane >= d) upto += v;
+        }
+        if (lane == kWave - 1) o.wave_sum[wave] = upto;
+        __syncthreads();
+        int before = all;
+        for (int w = 0; w < WAVES; ++w) {
+            if (w < wave) before += o.wave_sum[w];
+            all += o.wave_sum[w];
+        }
+        if (e < a.E) o.before[e] = before + upto - t;
+        __syncthreads();
+    }
+    if (tid == 0) o.before[a.E] = all;
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(all);
+}
+
+// Tile t: of `tiles_m` tiles of rows by tiles_n of UNITS outputs, an expert's
+// tiles of rows SIDE at a time beside each other for each tile of outputs.  Its
+// rows are spread evenly over its tiles, in 16s.
+template <int UNITS, int SIDE>
+__device__ __forceinline__ void locate(const Args& a, const Tiles& tiles, int tiles_m, uint32_t tiles_n, uint32_t t,
+                                       Where& o)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    int e = 0, first = 0, mt = tiles_m;
+    if (a.count != nullptr) {
+        // the last expert whose tiles start at or before t, in two probes
+        const int per = (a.E + kWave - 1) / kWave;
+        auto starts = [&](int i) { return i < a.E && (uint32_t)tiles.before[min(i, a.E)] * tiles_n <= t; };
+        const int g = (63 - (int)__builtin_clzll(__ballot(starts(lane * per)))) * per;
+        e = g + 63 - (int)__builtin_clzll(__ballot(lane < per && starts(g + lane)));
+        e = __builtin_amdgcn_readfirstlane(e);
+        first = __builtin_amdgcn_readfirstlane(tiles.before[e]);
+        mt = __builtin_amdgcn_readfirstlane(tiles.before[e + 1]) - first;
+    }
+    const uint32_t i = t - (uint32_t)first * tiles_n;
+    const uint32_t band = i / (SIDE * tiles_n), r = i - band * SIDE * tiles_n;
+    const uint32_t side = min((uint32_t)SIDE, (uint32_t)mt - band * SIDE);
+    const uint32_t m = band * SIDE + r % side;
+    int64_t row0;
+    const int64_t rows = rows_of(a, e, &row0, false), each = ((rows + 15) / 16 + mt - 1) / mt * 16;
+    const int64_t from = row0 + m * each, left = rows - m * each;
+    o.expert = e;
+    o.unit0 = (int)(r / side) * UNITS;
+    o.rows = __builtin_amdgcn_readfirstlane((int)(left < each ? left : each));
+    o.row0 = (int64_t)__builtin_amdgcn_readfirstlane((int)(from >> 32)) << 32 |
+             (uint32_t)__builtin_amdgcn_readfirstlane((int)from);
+}
+
+// ---- the tiled kernel -----------------------------------------------------------
+
 template <int BM, int BN, int WM, int WN, int S, bool GATE>
 __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S, GATE>::kBlocks)) void k_matmul(Args a)
 {
     using T = Tile<BM, BN, WM, WN, S, GATE>;
     constexpr int MT = T::MT, NT = T::NT;
     extern __shared__ __align__(1024) unsigned char smem[];     // stages, scales of two tiles
-    __shared__ int tile0[kMaxExperts + 1];      // tiles of rows before each expert
-    __shared__ int wave_sum[T::kWaves];
-
+    __shared__ Tiles tiles;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wm = wave % WM, wn = wave / WM;
     const int n = lane & 15, c = lane >> 4;
-    const bool grouped = a.count != nullptr;
-
-    // ---- which tiles there are
-    auto rows_of = [&](int e, int64_t* row0, bool flag) -> int64_t {
-        if (!grouped) {
-            *row0 = 0;
-            return a.num_rows;
-        }
-        int64_t r = a.count[e];
-        *row0 = a.psum[e];
-        if (a.cap > 0 && r > a.cap) r = a.cap;
-        if (*row0 + r > a.num_rows) {
-            r = *row0 < a.num_rows ? a.num_rows - *row0 : 0;
-            if (flag && blockIdx.x == 0) atomicOr(a.flags, kFlagCapacity);
-        }
-        return r;
-    };
-    int tiles_m = 0;
-    if (grouped) {
-        for (int e0 = 0; e0 < a.E; e0 += T::kThreads) {
-            const int e = e0 + tid;
-            int64_t row0;
-            const int t = e < a.E ? (int)((rows_of(e, &row0, true) + BM - 1) / BM) : 0;
-            int upto = t;
-#pragma unroll
-            for (int d = 1; d < kWave; d *= 2) {
-                const int v = __shfl_up(upto, d);
-                if (lane >= d) upto += v;
-            }
-            if (lane == kWave - 1) wave_sum[wave] = upto;
-            __syncthreads();
-            int before = tiles_m;
-            for (int w = 0; w < T::kWaves; ++w) {
-                if (w < wave) before += wave_sum[w];
-                tiles_m += wave_sum[w];
-            }
-            if (e < a.E) tile0[e] = before + upto - t;
-            __syncthreads();
-        }
-        if (tid == 0) tile0[a.E] = tiles_m;
-        __syncthreads();
-        tiles_m = __builtin_amdgcn_readfirstlane(tiles_m);
-    } else {
-        tiles_m = (int)((a.num_rows + BM - 1) / BM);
-    }
+    const int tiles_m = count_tiles<BM, T::kWaves>(a, tiles);
     const uint32_t tiles_n = (uint32_t)((a.units + T::kUnits - 1) / T::kUnits);
     const uint32_t total = (uint32_t)tiles_m * tiles_n;         // below 2^32: rows * outputs are below 2^35
     const uint32_t xcd = blockIdx.x % 8, stride = gridDim.x / 8;
@@ -181,32 +227,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
     at += blockIdx.x / 8;
     if (at >= stop) return;
 
-    auto locate = [&](uint32_t t, Where& o) {
-        int e = 0, first = 0, mt = tiles_m;
-        if (grouped) {
-            // the last expert whose tiles start at or before t, in two probes
-            const int per = (a.E + kWave - 1) / kWave;
-            auto starts = [&](int i) { return i < a.E && (uint32_t)tile0[min(i, a.E)] * tiles_n <= t; };
-            const int g = (63 - (int)__builtin_clzll(__ballot(starts(lane * per)))) * per;
-            e = g + 63 - (int)__builtin_clzll(__ballot(lane < per && starts(g + lane)));
-            e = __builtin_amdgcn_readfirstlane(e);
-            first = __builtin_amdgcn_readfirstlane(tile0[e]);
-            mt = __builtin_amdgcn_readfirstlane(tile0[e + 1]) - first;
-        }
-        const uint32_t i = t - (uint32_t)first * tiles_n;
-        constexpr uint32_t kSide = 4;
-        const uint32_t band = i / (kSide * tiles_n), r = i - band * kSide * tiles_n;
-        const uint32_t side = min(kSide, (uint32_t)mt - band * kSide);
-        const uint32_t m = band * kSide + r % side;
-        int64_t row0;
-        const int64_t rows = rows_of(e, &row0, false), each = ((rows + 15) / 16 + mt - 1) / mt * 16;
-        const int64_t from = row0 + m * each, left = rows - m * each;
-        o.expert = e;
-        o.unit0 = (int)(r / side) * T::kUnits;
-        o.rows = __builtin_amdgcn_readfirstlane((int)(left < each ? left : each));
-        o.row0 = (int64_t)__builtin_amdgcn_readfirstlane((int)(from >> 32)) << 32 |
-                 (uint32_t)__builtin_amdgcn_readfirstlane((int)from);
-    };
+    auto find = [&](uint32_t t, Where& o) { locate<T::kUnits, 4>(a, tiles, tiles_m, tiles_n, t, o); };
 
     const int steps = (a.cols + kStep - 1) / kStep;
 
@@ -221,7 +242,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
     unsigned char* const scales = smem + S * T::kStageBytes;
     auto aim = [&] {
         Where p;
-        locate(l_tile, p);
+        find(l_tile, p);
         xb = make_buffer(a.x + p.row0 * a.cols, (int64_t)p.rows * a.cols);
 #pragma unroll
         for (int j = 0; j < T::kXLoads; ++j) {
@@ -280,7 +301,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
 #pragma unroll 1
     for (int s = 0; s < S - 1; ++s) load_stage(s);
     Where p;
-    locate(at, p);
+    find(at, p);
     int live = (p.rows + 15) / 16, parity = 0;      // groups of rows; scales
     i32x4 acc[MT][NT];
 #pragma unroll
@@ -377,9 +398,110 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
         at += stride;
         if (at >= stop) return;
         parity ^= 1;
-        locate(at, p);
+        find(at, p);
         live = (p.rows + 15) / 16;
     }
+}
+
+// ---- few rows and outputs of one matrix --------------------------------------------
+//
+// A block has 16 outputs (16 gate and 16 up rows) of up to 16 rows; its waves take
+// the lines of 128 columns in turn, U of them in flight each, straight from memory
+// to registers, and add their sums in LDS (exact, so in any order).  What bounds it
+// is latency: the 29 MB of 7168 -> 4096 are 115 KB for each CU, and what counts is
+// that all of them are asked for at once.  One row 7.9 us (15 us with the few-row
+// kernel, whose 32-output tiles leave half of the CUs idle), 16 rows 10.2 (14.6).
+//
+// A load of weights takes 8 rows x 128 bytes (whole cache lines); of two, lanes
+// 0-7 and 8-15 of each row of 16 lanes trade one, which makes two operands: lane
+// (n, c) has bytes 32 c + 16 v of row n in operand v.
+__device__ __forceinline__ void trade_halves(const u32x4& a, const u32x4& b, i32x4& q0, i32x4& q1)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // row_ror:8, written in lanes 8-15 (banks 2, 3) or 0-7 (banks 0, 1)
+        q0[i] = __builtin_amdgcn_update_dpp((int)a[i], (int)b[i], 0x128, 0xF, 0xC, false);
+        q1[i] = __builtin_amdgcn_update_dpp((int)b[i], (int)a[i], 0x128, 0xF, 0x3, false);
+    }
+}
+
+__device__ __forceinline__ u32x4 load_line(Buffer b, uint32_t lane_off, uint32_t off)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_off, off, 0));
+}
+
+template <int U, bool GATE>
+__global__ __launch_bounds__(kThinWaves* kWave) void k_matmul_thin(Args a)
+{
+    constexpr int G = GATE ? 2 : 1;
+    __shared__ i32x4 sums[kThinWaves][G][kWave];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int n = lane & 15, c = lane >> 4;
+    const int unit0 = blockIdx.x * 16, have = min(16, a.units - unit0);
+    const int64_t row0 = (int64_t)blockIdx.y * 16;
+    const int rows = (int)min((int64_t)16, a.num_rows - row0);
+    Buffer wb[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+        wb[g] = make_buffer(a.w + ((int64_t)g * a.units + unit0) * a.cols, (int64_t)have * a.cols);
+    const Buffer xb = make_buffer(a.x + row0 * a.cols, (int64_t)rows * a.cols);
+    uint32_t wo[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const int r = 8 * v + (lane & 7);
+        wo[v] = r < have ? (uint32_t)r * (uint32_t)a.cols + 16u * (lane >> 3) : kNowhere;
+    }
+    const uint32_t xo = (uint32_t)n * (uint32_t)a.cols + 32u * c;
+
+    i32x4 acc[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) acc[g] = i32x4{0, 0, 0, 0};
+    const int lines = (a.cols + 127) / 128;
+    for (int l0 = wave; l0 < lines; l0 += kThinWaves * U) {
+        u32x4 w[U][G][2], x[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int line = l0 + u * kThinWaves, left = a.cols - line * 128;   // columns from it on
+            const uint32_t off = left > 0 ? (uint32_t)line * 128u : 0u;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) w[u][g][v] = load_line(wb[g], 16 * (lane >> 3) < left ? wo[v] : kNowhere, off);
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+                x[u][v] = load_line(xb, n < rows && 32 * c + 16 * v < left ? xo + 16u * v : kNowhere, off);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                i32x4 q[2];
+                trade_halves(w[u][g][0], w[u][g][1], q[0], q[1]);
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+                    acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(q[v], __builtin_bit_cast(i32x4, x[u][v]), acc[g], 0, 0, 0);
+            }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) sums[wave][g][lane] = acc[g];
+    __syncthreads();
+    // a lane of the first wave has outputs 4c to 4c + 3 of row n
+    const int u = unit0 + 4 * c;
+    if (wave != 0 || n >= rows || u >= a.units) return;
+    const float x1 = a.x_scales[row0 + n];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int w = 1; w < kThinWaves; ++w) acc[g] += sums[w][g][lane];
+    uint16_t* const to = a.y + (row0 + n) * a.units + u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (u + q < a.units) {
+            float v = (float)acc[0][q] * x1 * a.w_scales[u + q];
+            if constexpr (GATE) v = v / (1.f + __expf(-v)) * ((float)acc[1][q] * x1 * a.w_scales[a.units + u + q]);
+            to[q] = __builtin_bit_cast(uint16_t, (__bf16)v);
+        }
 }
 
 int num_cus()
@@ -394,12 +516,19 @@ int num_cus()
     return n;
 }
 
+// Tiles of BM rows that there can be: every expert may end in one of its own, and
+// each has a row.
+int64_t most_tiles(const Args& a, int64_t rows, int64_t bm)
+{
+    const int64_t n = (rows + bm - 1) / bm + (a.count ? a.E - 1 : 0);
+    return n < rows ? n : rows;
+}
+
 template <int BM, int BN, int WM, int WN, int S, bool GATE>
 hipError_t launch_tile(const Args& a, int64_t rows, hipStream_t s)
 {
     using T = Tile<BM, BN, WM, WN, S, GATE>;
-    // every expert may end in a tile of its own
-    const int64_t tiles = ((rows + BM - 1) / BM + (a.count ? a.E : 0)) * ((a.units + T::kUnits - 1) / T::kUnits);
+    const int64_t tiles = most_tiles(a, rows, BM) * ((a.units + T::kUnits - 1) / T::kUnits);
     const int64_t most = (int64_t)num_cus() / 8 * T::kBlocks, need = (tiles + 7) / 8;
     const dim3 grid((unsigned)(8 * (need < most ? need : most)));
     (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_matmul<BM, BN, WM, WN, S, GATE>),
@@ -408,11 +537,24 @@ hipError_t launch_tile(const Args& a, int64_t rows, hipStream_t s)
     return hipGetLastError();
 }
 
+template <int U, bool GATE>
+hipError_t launch_thin(const Args& a, int64_t rows, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.units + 15) / 16), (unsigned)((rows + 15) / 16));
+    hipLaunchKernelGGL((k_matmul_thin<U, GATE>), grid, dim3(kThinWaves * kWave), 0, s, a);
+    return hipGetLastError();
+}
+
 template <bool GATE>
 hipError_t launch_path(Path path, const Args& a, int64_t rows, hipStream_t s)
 {
     switch (path) {
-        case kPathTile64: return launch_tile<64, 128, 1, 4, stages(kPathTile64), GATE>(a, rows, s);
+        case kPathThin:
+            // two lines a wave at once if that is all there are: 2048 columns 4.4 us
+            // (4.7 with four), 7168 columns 8.5 (7.9)
+            return a.cols <= 2 * kThinWaves * 128 ? launch_thin<2, GATE>(a, rows, s) : launch_thin<4, GATE>(a, rows, s);
+        case kPathTile64x64: return launch_tile<64, 64, 2, 2, stages(kPathTile64x64), GATE>(a, rows, s);
+        case kPathTile64x128: return launch_tile<64, 128, 1, 4, stages(kPathTile64x128), GATE>(a, rows, s);
         case kPathTile128: return launch_tile<128, 128, 2, 2, stages(kPathTile128), GATE>(a, rows, s);
         default: return launch_tile<256, 256, 2, 4, stages(kPathTile256), GATE>(a, rows, s);
     }
@@ -424,7 +566,7 @@ hipError_t launch_path(Path path, const Args& a, int64_t rows, hipStream_t s)
 hipError_t launch_matmul(const ProductArgs& p, bool gate, hipStream_t s)
 {
     const int64_t rows = p.count ? p.P : p.num_rows, cols = 2 * (int64_t)p.w.cols;
-    const mm::Path path = mm::choose_path(gate, cols, p.units, p.count ? p.E : 1, rows);
+    const mm::Path path = mm::choose_path(gate, cols, p.units, p.count ? p.E : 0, rows);
     if (path == mm::kPathNone) return hipSuccess;
     if (path == mm::kPathFew) return launch_product_int8(p, gate ? kSwigluBf16 : kStoreBf16, s);
     mm::Args a = {};

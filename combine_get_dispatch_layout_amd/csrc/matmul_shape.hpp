@@ -8,35 +8,93 @@ namespace epk {
 namespace mm {
 
 constexpr int kStep = 128;          // columns of a step of the tiled kernels
+constexpr int kThinWaves = 8;       // waves of a block of the thin kernel
 
 enum Path {
-    kPathNone = 0,      // no rows
-    kPathFew = 1,       // the few-row kernels of product.hpp
-    kPathTile64 = 2,    // tiles of 64 rows x 128 outputs (64 with a gate)
-    kPathTile128 = 3,   // 128 x 128
-    kPathTile256 = 4    // 256 x 256
+    kPathNone = 0,          // no rows
+    kPathFew = 1,           // the few-row kernels of product.hpp
+    kPathThin = 2,          // one matrix, few rows and outputs
+    kPathTile64x64 = 3,     // tiles of 64 rows of x and 64 weight rows
+    kPathTile64x128 = 4,
+    kPathTile128 = 5,       // 128 x 128
+    kPathTile256 = 6        // 256 x 256
 };
 
-// Buffers of columns on their way (stages) of the tiled kernels.
-constexpr int stages(Path p) { return p == kPathTile64 ? 3 : 2; }
+// Buffers of columns on their way (stages) of the tiled kernels.  They hold the
+// scales of two tiles, so a tile has to have more steps than stages, lest those of
+// a third be on their way.
+constexpr int stages(Path p) { return p == kPathTile64x64 ? 4 : p == kPathTile64x128 ? 3 : 2; }
 
-// cols, rows of the weight matrix; experts: 1 for a dense product; rows: of all
+// The tiled kernels' time, in steps of a 256 x 256 tile (1.8 us): a step of a
+// round of tiles (one or two blocks to each CU) and what a round costs beside its
+// steps.  Measured, in us, with 7168 columns and no gate where one expert:
+//   rows x outputs          64x64  64x128  128x128  256x256
+//   64 x 4096                  21      30       37       64
+//   256 x 4096                 22      30       41       89
+//   512 x 4096                 26      31       41       89
+//   1024 x 4096                49      40       42       89
+//   2048 x 4096               101      83       60       91
+//   4096 x 4096                        155      113      100
+//   64 experts, 2048 columns, 2 x 768 outputs with the gate, rows an expert:
+//   16                         42      39       44       54
+//   64                         57      50       46       58
+//   128                        83      69       64       65
+//   256                       144     110       88       97
+//   512                       255     190      149      137
+struct TileCost {
+    Path path;
+    int bm, bn, at_once;    // blocks that 256 CUs hold
+    float alone, step;      // a step, with one block a CU and with all
+    float round;
+};
+constexpr TileCost kTileCosts[] = {
+    {kPathTile64x64, 64, 64, 512, 0.21f, 0.27f, 0.4f},
+    {kPathTile64x128, 64, 128, 512, 0.295f, 0.40f, 0.5f},
+    {kPathTile128, 128, 128, 512, 0.41f, 0.59f, 0.8f},
+    {kPathTile256, 256, 256, 256, 1.0f, 1.0f, 2.0f},
+};
+
+// cols, units of the weight matrix; experts: 0 for one matrix; rows: of all
 // experts.
 inline Path choose_path(bool gate, int64_t cols, int64_t units, int64_t experts, int64_t rows)
 {
     if (rows <= 0) return kPathNone;
+    const bool grouped = experts > 0;
+    if (!grouped) experts = 1;
     if (experts > rows) experts = rows;
     const int64_t likely = (rows + experts - 1) / experts;      // rows of an expert
-    // the tiled kernels keep the scales of two tiles, and a tile of fewer steps
-    // than that would have those of a third on their way
-    const int64_t steps = (cols + kStep - 1) / kStep;
-    if (likely <= 32 || steps <= stages(kPathTile64)) return kPathFew;
-    if (likely <= 64) return kPathTile64;
     const int64_t outputs = gate ? 2 * units : units;
-    const int64_t tiles256 = experts * ((likely + 255) / 256) * ((outputs + 255) / 256);
-    const int64_t tiles128 = experts * ((likely + 127) / 128) * ((outputs + 127) / 128);
-    if (likely >= 512 && tiles256 >= 256) return kPathTile256;
-    return tiles128 >= 512 ? kPathTile128 : kPathTile64;
+    const int64_t steps = (cols + kStep - 1) / kStep;
+    // the thin kernel's time follows its weight tiles of 16, 64 x 64 tiles' hardly
+    // does below 256: us with 7168 columns (and 2048), 1 to 16 rows:
+    //   tiles    256             512             896
+    //   thin     7.9-10 (4.5-5)  13-17 (6-7)     21-29 (10-13)
+    //   64 x 64  20     (7.8)    21    (7.8)     22    (8.0)
+    if (!grouped && rows <= 32 && (rows + 15) / 16 * ((units + 15) / 16) * (gate ? 2 : 1) <= 640) return kPathThin;
+    // decode batches of many experts: 256 experts, 7168 -> 2048, 4, 8, 12 rows an
+    // expert 554, 572, 668 us, with 64 x 128 tiles 610, 618, 626; 64 experts, 2048
+    // -> 2 x 768, 8 and 12 rows 37, 42, with tiles 38, 39
+    if (grouped && likely <= 8 && experts * ((outputs + 127) / 128) >= 512) return kPathFew;
+    Path best = kPathFew;
+    float least = 0.f;
+    for (const TileCost& t : kTileCosts) {
+        if (steps <= stages(t.path)) continue;
+        // an expert's tiles of rows: experts differ, so half a tile more where the
+        // mean is near a whole number of them
+        const float tiles_m = !grouped ? (float)((likely + t.bm - 1) / t.bm)
+                              : 10 * likely <= 8 * t.bm ? 1.f : (float)likely / t.bm + 0.5f;
+        const float fill = (float)likely / (tiles_m * t.bm);
+        const int64_t tiles = (int64_t)(tiles_m * experts + 0.5f) * ((outputs + t.bn - 1) / t.bn);
+        const int64_t whole = tiles / t.at_once, rest = tiles % t.at_once;
+        // half of a step's cost goes with the weights, half with the rows there are
+        const float step = whole * t.step + (rest == 0 ? 0.f : rest <= 256 ? t.alone : t.step);
+        const float cost = step * (0.5f + 0.5f * fill) * steps + (whole + (rest > 0 ? 1 : 0)) * t.round;
+        if (best == kPathFew || cost < least) {
+            best = t.path;
+            least = cost;
+        }
+    }
+    return best;
 }
 
 }  // namespace mm

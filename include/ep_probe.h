@@ -74,14 +74,16 @@ int ep_probe_product_path(int format, int group, int gate, int terms, int64_t co
  * kernels), 0 if it takes three; format, group: w_down's. */
 int ep_probe_layer_in_two(int format, int group, int64_t tokens, int64_t topk, int64_t inter);
 
-/* Which kernel serves a product of ep_matmul or ep_expert_matmul; arguments as
- * above, cols of the weight matrix. */
+/* Which kernel serves a product of ep_matmul (experts = 0) or ep_expert_matmul;
+ * other arguments as above, cols of the weight matrix. */
 enum {
-    EP_MATMUL_NONE = 0,     /* no rows                                         */
-    EP_MATMUL_FEW = 1,      /* the few-row kernels of ep_probe_product_path    */
-    EP_MATMUL_TILE64 = 2,   /* tiles of 64 rows                                */
-    EP_MATMUL_TILE128 = 3,  /* of 128                                          */
-    EP_MATMUL_TILE256 = 4   /* of 256                                          */
+    EP_MATMUL_NONE = 0,         /* no rows                                     */
+    EP_MATMUL_FEW = 1,          /* the kernels of ep_probe_product_path        */
+    EP_MATMUL_THIN = 2,         /* blocks of 16 rows and 16 outputs            */
+    EP_MATMUL_TILE64X64 = 3,    /* tiles of rows of x and weight rows          */
+    EP_MATMUL_TILE64X128 = 4,
+    EP_MATMUL_TILE128 = 5,
+    EP_MATMUL_TILE256 = 6
 };
 int ep_probe_matmul_path(int gate, int64_t cols, int64_t units, int64_t experts, int64_t rows);
 
