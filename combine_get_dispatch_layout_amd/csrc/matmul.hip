@@ -27,6 +27,15 @@
 // the blocks of an XCD (blockIdx % 8), which share an L2, work side by side: a
 // contiguous share of all tiles each, four tiles of rows by the tiles of outputs.
 //
+// Sums of integers may be taken in any order, so tiles of experts begin at a step
+// of their own and go round: blocks that start together would ask for the same
+// columns of rows a power of two apart, which lie in the same few channels of the
+// memory.  Where an expert has one tile of rows nothing is shared, and the tiles
+// of its outputs spread over all columns; with more, over four steps, so that they
+// still find each other's columns in L2.  128 experts of 45 rows, 4096 -> 1408:
+// 144 us, all from column 0 154 to 160; 64 of 768, 1536 -> 4096: 368 and 382;
+// 128 of 256, 2048 -> 2 x 768: 168 and 171; 7168 columns: equal to 1 % slower.
+//
 // What bounds it: power, and behind that the way through LDS.  4096 rows, 7168 ->
 // 4096 run at 1.8 GHz of 2.4.
 #include "experts.hpp"
@@ -112,6 +121,7 @@ struct Where {
     int expert, rows;
     int64_t row0;
     int unit0;
+    int m, side;                // its place among the tiles of rows beside each other
 };
 
 // ---- which tiles there are ------------------------------------------------------
@@ -193,7 +203,9 @@ __device__ __forceinline__ void locate(const Args& a, const Tiles& tiles, int ti
     const uint32_t i = t - (uint32_t)first * tiles_n;
     const uint32_t band = i / (SIDE * tiles_n), r = i - band * SIDE * tiles_n;
     const uint32_t side = min((uint32_t)SIDE, (uint32_t)mt - band * SIDE);
-    const uint32_t m = band * SIDE + r % side;
+    o.m = (int)(r % side);
+    o.side = (int)side;
+    const uint32_t m = band * SIDE + (uint32_t)o.m;
     int64_t row0;
     const int64_t rows = rows_of(a, e, &row0, false), each = ((rows + 15) / 16 + mt - 1) / mt * 16;
     const int64_t from = row0 + m * each, left = rows - m * each;
@@ -237,7 +249,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
     const int last_cols = a.cols - (steps - 1) * kStep;         // of the last step
     uint32_t xo[T::kXLoads], wo[T::kWLoads];
     Buffer xb, wb;
-    int l_step = 0, l_parity = 0;
+    int l_step = 0, l_k = 0, l_parity = 0;
     uint32_t l_tile = at;
     unsigned char* const scales = smem + S * T::kStageBytes;
     auto aim = [&] {
@@ -272,18 +284,25 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
             }
         }
         l_parity ^= 1;
+        // Where a tile's columns begin.  (One matrix: at 0, where blocks side by
+        // side share what they read; 4096 rows, 7168 -> 4096 102 us, turned 105.)
+        if (a.count != nullptr) {
+            const int turn = 3 * (p.unit0 / T::kUnits) + 2 * p.m;
+            l_k = turn % (p.side == 1 ? steps : min(4, steps));
+        }
     };
     auto load_stage = [&](int buf) {
         if (l_tile >= stop) return;
         unsigned char* const to = smem + buf * T::kStageBytes + wave * 1024;
-        const uint32_t k0 = (uint32_t)l_step * kStep;
-        const bool past = l_step == steps - 1 && 16 * l_piece >= last_cols;
+        const uint32_t k0 = (uint32_t)l_k * kStep;
+        const bool past = l_k == steps - 1 && 16 * l_piece >= last_cols;
 #pragma unroll
         for (int j = 0; j < T::kXLoads; ++j)
             load_to_lds(xb, to + j * T::kWaves * 1024, past ? kNowhere : xo[j], k0);
 #pragma unroll
         for (int j = 0; j < T::kWLoads; ++j)
             load_to_lds(wb, to + BM * kStep + j * T::kWaves * 1024, past ? kNowhere : wo[j], k0);
+        l_k = l_k == steps - 1 ? 0 : l_k + 1;
         if (++l_step == steps) {
             l_step = 0;
             l_tile += stride;
