@@ -230,16 +230,6 @@ __device__ __forceinline__ void add_up(const BalanceArgs& a, int64_t t0, int64_t
     constexpr int kLanes = kWave / X::kTokens;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    for (int e = tid; e < X::kMost; e += W * kWave) out.counts[e] = 0;
-    __syncthreads();
-    const int entries = (int)(t1 - t0) * a.K;
-    for (int i = tid; i < entries; i += W * kWave) {
-        const int t = a.k_magic ? (int)__umulhi((uint32_t)i, a.k_magic) : i;
-        if (a.mask && a.mask[t0 + t] == 0) continue;
-        const int e = a.topk[t0 * a.K + i];
-        if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&out.counts[e], 1);
-    }
-
     float acc[X::kEach], z[X::kEach], none[1];
 #pragma unroll
     for (int i = 0; i < X::kEach; ++i) acc[i] = 0.f;
@@ -249,7 +239,19 @@ __device__ __forceinline__ void add_up(const BalanceArgs& a, int64_t t0, int64_t
     auto counted = [&](int64_t t) { return t < t1 && (!a.mask || a.mask[t] != 0); };
     auto held = [&](int64_t t) { return t < t1 ? t : t0; };     // a token of the piece
     bool in = counted(mine);
+    // (before the counting, which waits for its own loads: 27.4 us against 28.4 for
+    // 65536 tokens of 256 experts; two to four tokens ahead take registers that
+    // four waves a SIMD need, 29 to 34)
     if (t0 < t1) X::load(a, held(mine), next);
+    for (int e = tid; e < X::kMost; e += W * kWave) out.counts[e] = 0;
+    __syncthreads();
+    const int entries = (int)(t1 - t0) * a.K;
+    for (int i = tid; i < entries; i += W * kWave) {
+        const int t = a.k_magic ? (int)__umulhi((uint32_t)i, a.k_magic) : i;
+        if (a.mask && a.mask[t0 + t] == 0) continue;
+        const int e = a.topk[t0 * a.K + i];
+        if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&out.counts[e], 1);
+    }
     for (int64_t t = mine; t - lane / kLanes < t1; t += W * X::kTokens) {
         const bool now = in;
         X::unpack(a, next, z);
