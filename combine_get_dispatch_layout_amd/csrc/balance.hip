@@ -28,8 +28,8 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 
-// Waves of a block of the second kernel, at most.
-constexpr int kFinishWaves = 16;
+// The second kernel: waves of a block and blocks, at most.
+constexpr int kFinishWaves = 16, kFinishBlocks = 256;
 
 // A chunk: at least 16 tokens (four waves of four), so many that some 1024
 // blocks make the batch, at most 1024 (which bounds the fp32 sums' length).
@@ -285,11 +285,16 @@ __global__ __launch_bounds__(kThreads) void k_balance_pieces(BalanceArgs a)
     const int64_t c0 = (int64_t)blockIdx.x * a.chunk;
     const int64_t c1 = c0 + a.chunk < a.N ? c0 + a.chunk : a.N;
 
-    for (int q = a.start ? first_sequence(a, c0) : 0; q < a.Q; ++q) {
+    for (int q = a.start ? first_sequence(a, c0) : 0, next = q + 1; q < a.Q; q = next++) {
         const int64_t s0 = a.start ? start_of(a, q) : 0, s1 = a.start ? start_of(a, (int64_t)q + 1) : a.N;
         if (s0 >= c1) break;
         const int64_t t0 = s0 > c0 ? s0 : c0, t1 = s1 < c1 ? s1 : c1;
-        if (t0 >= t1) continue;
+        if (t0 >= t1) {
+            // empty, as its neighbours may be: on to the next that ends behind here
+            // (one by one, 1000 that pad a batch cost 400 us)
+            next = max(first_sequence(a, t0), next);
+            continue;
+        }
         add_up<X, kWaves>(a, t0, t1, piece);
         const int64_t slot = (int64_t)blockIdx.x + q;
         for (int e = tid; e < a.E; e += kThreads) {
@@ -346,59 +351,84 @@ __device__ __forceinline__ int wave_total(int v)
     return v;
 }
 
-// Adds up a sequence's pieces for 64 experts, one a lane, each wave every
-// `waves`-th piece; the last block to finish adds up the blocks' shares of the
-// loss, in their order.  A chain of loads and one barrier.
-__global__ __launch_bounds__(kFinishWaves* kWave) void k_balance_finish(BalanceArgs a, int slices)
+// Adds up the pieces: an item is a sequence's 64 experts, one a lane, by `join`
+// waves, each every join-th piece.  A block has waves / join items at a time and
+// goes on by the whole grid's; the last block to finish adds up the blocks' shares
+// of the loss, in their order.  What bounds it is a chain of loads, and with many
+// blocks their way past the one counter, 23 ns each: 65536 tokens of 256 experts in
+// 1024 sequences took 131 us with a block an item, 29 with at most 256 blocks (both
+// kernels), in 8192 sequences 807 and 60.
+__global__ __launch_bounds__(kFinishWaves* kWave) void k_balance_finish(BalanceArgs a, int slices, int join)
 {
     __shared__ double sums[kFinishWaves][kWave];
     __shared__ int counts[kFinishWaves][kWave];
+    __shared__ double shares[kFinishWaves];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), waves = blockDim.x / kWave;
-    const int q = blockIdx.x / slices, e = (blockIdx.x % slices) * kWave + lane;
-    const int64_t s0 = a.start ? start_of(a, q) : 0, s1 = a.start ? start_of(a, (int64_t)q + 1) : a.N;
-    const int64_t first = s0 / a.chunk, pieces = s1 > s0 ? (s1 - 1) / a.chunk - first + 1 : 0;
-    const int64_t slot0 = first + q;
+    const int part = wave % join, at_once = waves / join;
+    const int items = a.Q * slices, stride = (int)gridDim.x * at_once;      // below 2^23
+    double shared = 0.0;        // the wave's items' shares of the loss
+    for (int i0 = (int)blockIdx.x * at_once; i0 < items; i0 += stride) {
+        const int item = i0 + wave / join;
+        const bool there = item < items;
+        const int q = there ? item / slices : 0, slice = item % slices, e = slice * kWave + lane;
+        // (tokens are below 2^31)
+        const uint32_t s0 = a.start ? (uint32_t)start_of(a, q) : 0u;
+        const uint32_t s1 = a.start ? (uint32_t)start_of(a, (int64_t)q + 1) : (uint32_t)a.N;
+        const int first = (int)(s0 / (uint32_t)a.chunk);
+        const int pieces = there && s1 > s0 ? (int)((s1 - 1) / (uint32_t)a.chunk) - first + 1 : 0;
+        const int64_t slot0 = (int64_t)first + q;
 
-    int live = 0;
-    if (wave == 0)
-        for (int64_t i = lane; i < pieces; i += kWave) live += a.part_tokens[slot0 + i];
-    double sum = 0.0;
-    int count = 0;
-    if (e < a.E)
+        int live = 0;
+        if (part == 0)
+            for (int i = lane; i < pieces; i += kWave) live += a.part_tokens[slot0 + i];
+        double sum = 0.0;
+        int count = 0;
+        if (e < a.E)
 #pragma unroll 8
-        for (int64_t i = wave; i < pieces; i += waves) {
-            sum += (double)a.part_sum[(slot0 + i) * a.E + e];
-            count += a.part_count[(slot0 + i) * a.E + e];
+            for (int i = part; i < pieces; i += join) {
+                sum += (double)a.part_sum[(slot0 + i) * a.E + e];
+                count += a.part_count[(slot0 + i) * a.E + e];
+            }
+        if (join > 1) {
+            sums[wave][lane] = sum;
+            counts[wave][lane] = count;
+            __syncthreads();
+            if (part == 0)
+                for (int w = 1; w < join; ++w) {
+                    sum += sums[wave + w][lane];
+                    count += counts[wave + w][lane];
+                }
+            if (i0 + stride < items) __syncthreads();
         }
-    sums[wave][lane] = sum;
-    counts[wave][lane] = count;
-    __syncthreads();
+        if (part != 0 || !there) continue;
+        live = wave_total(live);
+        if (e < a.E) {
+            a.sums[(int64_t)q * a.E + e] = (float)sum;
+            a.counts[(int64_t)q * a.E + e] = count;
+        }
+        if (slice == 0 && lane == 0) a.tokens[q] = live;
+        const double dot = wave_sum(sum * (double)count);
+        if (live > 0) shared += a.factor * dot / ((double)live * (double)live);
+    }
+    if (at_once > 1) {
+        if (lane == 0) shares[wave] = shared;
+        __syncthreads();
+    }
     if (wave != 0) return;
-    for (int w = 1; w < waves; ++w) {
-        sum += sums[w][lane];
-        count += counts[w][lane];
-    }
-    live = wave_total(live);
-    if (e < a.E) {
-        a.sums[(int64_t)q * a.E + e] = (float)sum;
-        a.counts[(int64_t)q * a.E + e] = count;
-    }
-    if (blockIdx.x % slices == 0 && lane == 0) a.tokens[q] = live;
-    const double dot = wave_sum(sum * (double)count);
-    const double share = live > 0 ? a.factor * dot / ((double)live * (double)live) : 0.0;
+    for (int w = join; w < waves; w += join) shared += shares[w];
     const int blocks = (int)gridDim.x;
     if (blocks == 1) {
-        if (lane == 0) *a.loss = (float)share;
+        if (lane == 0) *a.loss = (float)shared;
         return;
     }
     uint32_t before = 0;
     if (lane == 0) {
-        __hip_atomic_store(&a.part_loss[blockIdx.x], share, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&a.part_loss[blockIdx.x], shared, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         before = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
     }
     if (__builtin_amdgcn_readfirstlane((int)before) != blocks - 1) return;
-    sum = 0.0;
+    double sum = 0.0;
     for (int i = lane; i < blocks; i += kWave)
         sum += __hip_atomic_load(&a.part_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     sum = wave_sum(sum);
@@ -445,9 +475,19 @@ __global__ __launch_bounds__(kThreads) void k_balance_backward(BalanceArgs a)
         coming = unmasked(t + kWaves * X::kTokens);
         X::load(a, held(t + kWaves * X::kTokens), next);
         if (t >= c1) continue;
-        while (q < a.Q && s1 <= t) {
+        if (q < a.Q && s1 <= t) {
             ++q;
             bounds();
+            if (q < a.Q && s1 <= t) {       // empty ones: the next that ends behind t
+                int lo = q + 1, hi = a.Q;
+                while (lo < hi) {
+                    const int mid = lo + (hi - lo) / 2;
+                    if (start_of(a, (int64_t)mid + 1) > t) hi = mid;
+                    else lo = mid + 1;
+                }
+                q = lo;
+                bounds();
+            }
         }
         const bool in = live && q < a.Q && s0 <= t;
         if (in && q != loaded) {
@@ -555,10 +595,13 @@ BalanceCarve carve_balance(int64_t N, int E, int Q)
     BalanceCarve c;
     c.chunk = chunk_of(N);
     c.slots = (N + c.chunk - 1) / c.chunk + Q;
-    c.blocks = (int64_t)Q * ((E + kWave - 1) / kWave);
-    // as many waves as a sequence has pieces to go round, eight each
-    const int64_t waves = (c.slots / Q + 7) / 8;
-    c.waves = (int)(waves < 1 ? 1 : waves < kFinishWaves ? waves : kFinishWaves);
+    // as many waves join as a sequence has pieces to go round, eight each
+    const int64_t join = (c.slots / Q + 7) / 8, items = (int64_t)Q * ((E + kWave - 1) / kWave);
+    c.join = (int)(join < 1 ? 1 : join < kFinishWaves ? join : kFinishWaves);
+    c.at_once = kFinishWaves / c.join;
+    if (c.at_once > items) c.at_once = (int)items;
+    c.blocks = (items + c.at_once - 1) / c.at_once;
+    if (c.blocks > kFinishBlocks) c.blocks = kFinishBlocks;
     c.sum = 0;
     c.count = c.sum + up(4 * c.slots * E);
     c.tokens = c.count + up(4 * c.slots * E);
@@ -572,8 +615,8 @@ hipError_t launch_balance(const BalanceArgs& a, const BalanceCarve& c, hipStream
 {
     const hipError_t e = launch_any<false>(a, s);
     if (e != hipSuccess || is_small(a)) return e;
-    hipLaunchKernelGGL(k_balance_finish, dim3((unsigned)c.blocks), dim3(c.waves * kWave), 0, s, a,
-                       (int)(c.blocks / a.Q));
+    hipLaunchKernelGGL(k_balance_finish, dim3((unsigned)c.blocks), dim3(c.at_once * c.join * kWave), 0, s, a,
+                       (a.E + kWave - 1) / kWave, c.join);
     return hipGetLastError();
 }
 

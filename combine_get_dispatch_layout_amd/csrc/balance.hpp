@@ -40,8 +40,10 @@ struct BalanceArgs {
 // Workspace of the forward kernels, in bytes from its start.
 struct BalanceCarve {
     int chunk;
-    int64_t slots, blocks;      // blocks of the second kernel
-    int waves;                  // of a block of it
+    int64_t slots;
+    // of the second kernel: blocks, items of a block at a time, waves of an item
+    int64_t blocks;
+    int at_once, join;
     int64_t sum, count, tokens, loss, ticket, total;
 };
 BalanceCarve carve_balance(int64_t N, int E, int Q);

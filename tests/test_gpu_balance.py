@@ -178,6 +178,42 @@ def test_large_batch():
     check(z, idx)
 
 
+@pytest.mark.parametrize("N,E,real,padded", [(300, 24, 6, 3000), (2000, 64, 37, 5000), (1100, 256, 9, 1100)])
+def test_padded_sequences(N, E, real, padded):
+    """Many empty sequences in one place: behind the last, before the first,
+    between two, with tokens of no sequence beside them."""
+    say(f"[balance padded] {N} {E} {real} {padded}")
+    z, idx, mask, _ = inputs(N, E, 4, masked=0.1)
+    some = np.sort(np.random.default_rng(5).integers(N // 10, N - N // 10, real + 1)).astype(np.int32)
+    for k in (real, 0, real // 2):
+        start = np.insert(some, k, np.full(padded, some[k]))
+        check(z, idx, mask, start)
+        check(z, idx, None, start, "sigmoid", False, dtype=torch.bfloat16)
+
+
+def test_long_sequences_by_the_thousand():
+    """Sequences of several pieces each, more of them than the second kernel's
+    blocks hold at a time.  The relative error of a sum of scores is below 128 u:
+    |a| <= 16 and 32 of a score, 64 + 6 of the sums (balance_reference); the
+    second kernel's are in 64 bits, its result is rounded once."""
+    N, E, Q = 15_000_000, 4, 2049
+    say(f"[balance long] {N} {E} {Q}")
+    gen = torch.Generator("cuda").manual_seed(3)
+    lg = torch.randn((N, E), device="cuda", generator=gen)
+    idx = lg.argmax(1, keepdim=True).int()
+    start = torch.linspace(0, N, Q + 1, dtype=torch.float64).round().int().cuda()
+    out = moe.ep_balance_loss(moe.BalanceConfig(E, 1, coefficient=0.5), lg, idx, None, start)
+    lens = start.diff().long()
+    p = torch.softmax(lg.double(), 1)
+    of = torch.repeat_interleave(torch.arange(Q, device="cuda"), lens)
+    S = torch.zeros((Q, E), dtype=torch.float64, device="cuda").index_add_(0, of, p)
+    n = torch.bincount(of * E + idx[:, 0], minlength=Q * E).view(Q, E)
+    assert torch.equal(out.counts.long(), n) and torch.equal(out.seq_tokens.long(), lens)
+    assert ((out.score_sums.double() - S).abs() <= 129 * B.U * S).all()
+    loss = 0.5 / Q * (E / lens.double() ** 2 * (n * S).sum(1)).sum()
+    assert abs(float(out.loss) - float(loss)) <= 129 * B.U * float(loss)
+
+
 def test_counts_of_all_ranks():
     """The gradient takes counts and tokens summed over ranks."""
     z, idx, _, _ = inputs(64, 32, 4)
