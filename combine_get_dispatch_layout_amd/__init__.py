@@ -13,7 +13,8 @@ from .ep import (Config, EpError, Handle, ep_check_error, ep_combine, ep_dispatc
                  EP_QUANT_INT8, EP_QUANT_MXFP4, EP_SCALE_FP32, EP_SCALE_POW2, EP_SCALE_UE8M0)
 from .moe import (Balance, BalanceConfig, GateConfig, Weights, ep_balance_loss,  # noqa: F401
                   ep_balance_loss_backward, ep_balance_workspace_size, ep_expert_matmul,
-                  ep_expert_matvec, ep_gate, ep_gate_backward, ep_matmul, ep_matvec, ep_moe_layer,
+                  ep_expert_matvec, ep_gate, ep_gate_backward, ep_matmul,
+                  ep_matmul_workspace_size, ep_matvec, ep_moe_layer,
                   ep_moe_workspace_size, EP_ACT_NONE, EP_ACT_SWIGLU, EP_SCORE_SIGMOID,
                   EP_SCORE_SOFTMAX, EP_WEIGHT_BF16, EP_WEIGHT_INT4, EP_WEIGHT_INT8,
                   EP_WEIGHT_MXFP4)

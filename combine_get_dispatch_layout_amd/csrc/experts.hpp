@@ -92,7 +92,9 @@ hipError_t launch_product(ProductArgs a, int epilogue, hipStream_t s);
 // where the batch is small enough for it (*done).
 hipError_t launch_down_few(const ProductArgs& a, bool* done, hipStream_t s);
 // Products in 8-bit integers (kInt8): y = bf16, gated or not.
-hipError_t launch_matmul(const ProductArgs& a, bool gate, hipStream_t s);
+// part: room for matmul_workspace bytes of sums, or null (one kernel then).
+hipError_t launch_matmul(const ProductArgs& a, bool gate, int32_t* part, hipStream_t s);
+int64_t matmul_workspace(bool gate, int64_t cols, int64_t units, int64_t rows);
 hipError_t launch_layer_reduce(const ReduceArgs& a, hipStream_t s);
 hipError_t launch_gate(const GateArgs& a, hipStream_t s);
 hipError_t launch_gate_backward(const GateArgs& a, hipStream_t s);

@@ -27,14 +27,17 @@
 // the blocks of an XCD (blockIdx % 8), which share an L2, work side by side: a
 // contiguous share of all tiles each, four tiles of rows by the tiles of outputs.
 //
-// Sums of integers may be taken in any order, so tiles of experts begin at a step
-// of their own and go round: blocks that start together would ask for the same
+// Sums of integers may be taken in any order, so tiles of experts, or of one matrix
+// and few rows, begin at a step of their own and go round: blocks that start together would ask for the same
 // columns of rows a power of two apart, which lie in the same few channels of the
 // memory.  Where an expert has one tile of rows nothing is shared, and the tiles
 // of its outputs spread over all columns; with more, over four steps, so that they
 // still find each other's columns in L2.  128 experts of 45 rows, 4096 -> 1408:
 // 144 us, all from column 0 154 to 160; 64 of 768, 1536 -> 4096: 368 and 382;
 // 128 of 256, 2048 -> 2 x 768: 168 and 171; 7168 columns: equal to 1 % slower.
+//
+// Where tiles are fewer than CUs, their columns are split over blocks if the caller
+// has room for the sums, which a second kernel joins (choose_splits).
 //
 // What bounds it: power, and behind that the way through LDS.  4096 rows, 7168 ->
 // 4096 run at 1.8 GHz of 2.4.
@@ -65,6 +68,8 @@ struct Args {
     const int32_t* count;
     int cap;
     uint16_t* y;                // [.., units]
+    int splits;                 // of the columns, and their sums [splits, num_rows, rows]
+    int32_t* part;
     uint32_t* flags;
 };
 
@@ -122,6 +127,7 @@ struct Where {
     int64_t row0;
     int unit0;
     int m, side;                // its place among the tiles of rows beside each other
+    int split, first, steps;    // its steps
 };
 
 // ---- which tiles there are ------------------------------------------------------
@@ -218,7 +224,7 @@ __device__ __forceinline__ void locate(const Args& a, const Tiles& tiles, int ti
 
 // ---- the tiled kernel -----------------------------------------------------------
 
-template <int BM, int BN, int WM, int WN, int S, bool GATE>
+template <int BM, int BN, int WM, int WN, int S, bool GATE, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S, GATE>::kBlocks)) void k_matmul(Args a)
 {
     using T = Tile<BM, BN, WM, WN, S, GATE>;
@@ -231,7 +237,8 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
     const int n = lane & 15, c = lane >> 4;
     const int tiles_m = count_tiles<BM, T::kWaves>(a, tiles);
     const uint32_t tiles_n = (uint32_t)((a.units + T::kUnits - 1) / T::kUnits);
-    const uint32_t total = (uint32_t)tiles_m * tiles_n;         // below 2^32: rows * outputs are below 2^35
+    const uint32_t whole = (uint32_t)tiles_m * tiles_n;         // below 2^32: rows * outputs are below 2^35
+    const uint32_t total = SPLIT ? whole * (uint32_t)a.splits : whole;
     const uint32_t xcd = blockIdx.x % 8, stride = gridDim.x / 8;
     const uint32_t share = total / 8, more = total % 8;
     uint32_t at = xcd * share + min(xcd, more);
@@ -239,9 +246,17 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
     at += blockIdx.x / 8;
     if (at >= stop) return;
 
-    auto find = [&](uint32_t t, Where& o) { locate<T::kUnits, 4>(a, tiles, tiles_m, tiles_n, t, o); };
-
     const int steps = (a.cols + kStep - 1) / kStep;
+    // a tile; SPLIT: and its share of the steps
+    auto find = [&](uint32_t t, Where& o) {
+        if constexpr (SPLIT) {
+            o.split = (int)(t / whole);
+            o.first = o.split * steps / a.splits;
+            o.steps = (o.split + 1) * steps / a.splits - o.first;
+            t %= whole;
+        }
+        locate<T::kUnits, 4>(a, tiles, tiles_m, tiles_n, t, o);
+    };
 
     // ---- loads, S - 1 stages ahead of the arithmetic
     const int l_row = lane / 8, l_piece = lane % 8 ^ l_row;
@@ -249,7 +264,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
     const int last_cols = a.cols - (steps - 1) * kStep;         // of the last step
     uint32_t xo[T::kXLoads], wo[T::kWLoads];
     Buffer xb, wb;
-    int l_step = 0, l_k = 0, l_parity = 0;
+    int l_step = 0, l_k = 0, l_first = 0, l_steps = 0, l_parity = 0;
     uint32_t l_tile = at;
     unsigned char* const scales = smem + S * T::kStageBytes;
     auto aim = [&] {
@@ -270,25 +285,33 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
             const int u = GATE ? r / 32 * 16 + r % 16 : r;
             wo[j] = u < have ? (uint32_t)u * (uint32_t)a.cols + 16u * l_piece : kNowhere;
         }
-        // scales of its rows, then of its outputs in the order of the groups
-        const Buffer xs = make_buffer(a.x_scales + p.row0, 4 * (int64_t)p.rows);
-        const Buffer ws = make_buffer(a.w_scales + (int64_t)p.expert * a.rows, 4 * (int64_t)a.rows);
-        for (int q = wave; q < T::kScaleLoads; q += T::kWaves) {
-            unsigned char* const to = scales + l_parity * T::kScaleBytes + q * 256;
-            if (q < BM / 64) {
-                load_word_to_lds(xs, to, (uint32_t)(q * 64 + lane) * 4);
-            } else {
-                const int r = (q - BM / 64) * 64 + lane;
-                const int u = p.unit0 + (GATE ? r / 32 * 16 + r % 16 : r);
-                load_word_to_lds(ws, to, u < a.units ? (uint32_t)(u + (GATE && r / 16 % 2 ? a.units : 0)) * 4 : kNowhere);
+        if constexpr (!SPLIT) {
+            // scales of its rows, then of its outputs in the order of the groups
+            const Buffer xs = make_buffer(a.x_scales + p.row0, 4 * (int64_t)p.rows);
+            const Buffer ws = make_buffer(a.w_scales + (int64_t)p.expert * a.rows, 4 * (int64_t)a.rows);
+            for (int q = wave; q < T::kScaleLoads; q += T::kWaves) {
+                unsigned char* const to = scales + l_parity * T::kScaleBytes + q * 256;
+                if (q < BM / 64) {
+                    load_word_to_lds(xs, to, (uint32_t)(q * 64 + lane) * 4);
+                } else {
+                    const int r = (q - BM / 64) * 64 + lane;
+                    const int u = p.unit0 + (GATE ? r / 32 * 16 + r % 16 : r);
+                    load_word_to_lds(ws, to, u < a.units ? (uint32_t)(u + (GATE && r / 16 % 2 ? a.units : 0)) * 4 : kNowhere);
+                }
             }
+            l_parity ^= 1;
         }
-        l_parity ^= 1;
-        // Where a tile's columns begin.  (One matrix: at 0, where blocks side by
-        // side share what they read; 4096 rows, 7168 -> 4096 102 us, turned 105.)
-        if (a.count != nullptr) {
+        // Where a tile's columns begin.  (One matrix of many rows: at 0, where blocks
+        // side by side share what they read; 4096 rows, 7168 -> 4096 102 us, turned
+        // 105.  Of few rows: 64 rows, 4096 -> 65536 turned 51 us, all from 0 63.)
+        if constexpr (SPLIT) {
+            l_first = l_k = p.first;
+            l_steps = p.steps;
+        }
+        if (a.count != nullptr || tiles_m == 1) {
             const int turn = 3 * (p.unit0 / T::kUnits) + 2 * p.m;
-            l_k = turn % (p.side == 1 ? steps : min(4, steps));
+            if constexpr (SPLIT) l_k = l_first + turn % l_steps;
+            else l_k = turn % (p.side == 1 ? steps : min(4, steps));
         }
     };
     auto load_stage = [&](int buf) {
@@ -302,8 +325,9 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
 #pragma unroll
         for (int j = 0; j < T::kWLoads; ++j)
             load_to_lds(wb, to + BM * kStep + j * T::kWaves * 1024, past ? kNowhere : wo[j], k0);
-        l_k = l_k == steps - 1 ? 0 : l_k + 1;
-        if (++l_step == steps) {
+        if constexpr (SPLIT) l_k = l_k == l_first + l_steps - 1 ? l_first : l_k + 1;
+        else l_k = l_k == steps - 1 ? 0 : l_k + 1;
+        if (++l_step == (SPLIT ? l_steps : steps)) {
             l_step = 0;
             l_tile += stride;
             if (l_tile < stop) aim();
@@ -353,61 +377,84 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
                 }
         }
         buf = buf == S - 1 ? 0 : buf + 1;
-        if (++step < steps) continue;
+        if (++step < (SPLIT ? p.steps : steps)) continue;
         step = 0;
 
-        // ---- store: this lane has outputs 4c .. 4c+3 of row n of each group
-        constexpr int NO = GATE ? NT / 2 : NT;      // groups of outputs
-        const float* const xs = reinterpret_cast<const float*>(scales + parity * T::kScaleBytes) + n;
-        const f32x4* const ws =
-            reinterpret_cast<const f32x4*>(scales + parity * T::kScaleBytes + 4 * BM) + wn * NT * 4 + c;
-        f32x4 w4[NT];
+        if constexpr (SPLIT) {
+            // the sums as they are, in the order of the weight rows
 #pragma unroll
-        for (int j = 0; j < NT; ++j) w4[j] = ws[j * 4];
-        const int u0 = p.unit0 + wn * NO * 16;
+            for (int i = 0; i < MT; ++i) {
+                const int m = (i * WM + wm) * 16 + n;
+                if (m >= p.rows) continue;
+                int32_t* const to = a.part + ((int64_t)p.split * a.num_rows + p.row0 + m) * a.rows;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int m = (i * WM + wm) * 16 + n;
-            if ((i * WM + wm) * 16 >= p.rows) continue;
-            const float x1 = xs[(i * WM + wm) * 16];
-            uint32_t lo[NO], hi[NO];
+                for (int j = 0; j < NT; ++j) {
+                    const int g = wn * NT + j;
+                    const int u = p.unit0 + (GATE ? g / 2 : g) * 16 + 4 * c;
+                    int32_t* const at4 = to + u + (GATE && g % 2 ? a.units : 0);
+                    if (a.vec) {
+                        if (u < a.units) *reinterpret_cast<i32x4*>(at4) = acc[i][j];
+                    } else {
 #pragma unroll
-            for (int o = 0; o < NO; ++o) {
-                float v[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    v[q] = (float)acc[i][GATE ? 2 * o : o][q] * x1 * w4[GATE ? 2 * o : o][q];
-                    // (the exponential is good to 2^-24 of its argument)
-                    if constexpr (GATE)
-                        v[q] = v[q] / (1.f + __expf(-v[q])) * ((float)acc[i][2 * o + 1][q] * x1 * w4[2 * o + 1][q]);
+                        for (int q = 0; q < 4; ++q)
+                            if (u + q < a.units) at4[q] = acc[i][j][q];
+                    }
                 }
-                const u32x2 d = __builtin_bit_cast(u32x2, __builtin_convertvector(f32x4{v[0], v[1], v[2], v[3]}, bf16x4));
-                lo[o] = d[0];
-                hi[o] = d[1];
             }
-            uint16_t* const to = a.y + (p.row0 + m) * a.units;
-            if (a.vec) {
-                // two groups: their lanes trade, 8 outputs of one group each
+        } else {
+            // ---- store: this lane has outputs 4c .. 4c+3 of row n of each group
+            constexpr int NO = GATE ? NT / 2 : NT;      // groups of outputs
+            const float* const xs = reinterpret_cast<const float*>(scales + parity * T::kScaleBytes) + n;
+            const f32x4* const ws =
+                reinterpret_cast<const f32x4*>(scales + parity * T::kScaleBytes + 4 * BM) + wn * NT * 4 + c;
+            f32x4 w4[NT];
 #pragma unroll
-                for (int o = 0; o + 1 < NO; o += 2) {
-                    swap16(lo[o], lo[o + 1]);
-                    swap16(hi[o], hi[o + 1]);
-                    const int u = u0 + (o + c % 2) * 16 + c / 2 * 8;
-                    if (m < p.rows && u < a.units)
-                        *reinterpret_cast<u32x4*>(to + u) = u32x4{lo[o], hi[o], lo[o + 1], hi[o + 1]};
-                }
-                if constexpr (NO % 2 != 0) {
-                    const int u = u0 + (NO - 1) * 16 + 4 * c;
-                    if (m < p.rows && u < a.units) *reinterpret_cast<u32x2*>(to + u) = u32x2{lo[NO - 1], hi[NO - 1]};
-                }
-            } else if (m < p.rows) {
+            for (int j = 0; j < NT; ++j) w4[j] = ws[j * 4];
+            const int u0 = p.unit0 + wn * NO * 16;
 #pragma unroll
-                for (int o = 0; o < NO; ++o)
+            for (int i = 0; i < MT; ++i) {
+                const int m = (i * WM + wm) * 16 + n;
+                if ((i * WM + wm) * 16 >= p.rows) continue;
+                const float x1 = xs[(i * WM + wm) * 16];
+                uint32_t lo[NO], hi[NO];
+#pragma unroll
+                for (int o = 0; o < NO; ++o) {
+                    float v[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int u = u0 + o * 16 + 4 * c + q;
-                        if (u < a.units) to[u] = (uint16_t)((q < 2 ? lo[o] : hi[o]) >> (q % 2 * 16));
+                        v[q] = (float)acc[i][GATE ? 2 * o : o][q] * x1 * w4[GATE ? 2 * o : o][q];
+                        // (the exponential is good to 2^-24 of its argument)
+                        if constexpr (GATE)
+                            v[q] = v[q] / (1.f + __expf(-v[q])) * ((float)acc[i][2 * o + 1][q] * x1 * w4[2 * o + 1][q]);
                     }
+                    const u32x2 d = __builtin_bit_cast(u32x2, __builtin_convertvector(f32x4{v[0], v[1], v[2], v[3]}, bf16x4));
+                    lo[o] = d[0];
+                    hi[o] = d[1];
+                }
+                uint16_t* const to = a.y + (p.row0 + m) * a.units;
+                if (a.vec) {
+                    // two groups: their lanes trade, 8 outputs of one group each
+#pragma unroll
+                    for (int o = 0; o + 1 < NO; o += 2) {
+                        swap16(lo[o], lo[o + 1]);
+                        swap16(hi[o], hi[o + 1]);
+                        const int u = u0 + (o + c % 2) * 16 + c / 2 * 8;
+                        if (m < p.rows && u < a.units)
+                            *reinterpret_cast<u32x4*>(to + u) = u32x4{lo[o], hi[o], lo[o + 1], hi[o + 1]};
+                    }
+                    if constexpr (NO % 2 != 0) {
+                        const int u = u0 + (NO - 1) * 16 + 4 * c;
+                        if (m < p.rows && u < a.units) *reinterpret_cast<u32x2*>(to + u) = u32x2{lo[NO - 1], hi[NO - 1]};
+                    }
+                } else if (m < p.rows) {
+#pragma unroll
+                    for (int o = 0; o < NO; ++o)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int u = u0 + o * 16 + 4 * c + q;
+                            if (u < a.units) to[u] = (uint16_t)((q < 2 ? lo[o] : hi[o]) >> (q % 2 * 16));
+                        }
+                }
             }
         }
 #pragma unroll
@@ -523,6 +570,46 @@ __global__ __launch_bounds__(kThinWaves* kWave) void k_matmul_thin(Args a)
         }
 }
 
+// Joins the sums of tiles whose columns were split over blocks: four outputs of a
+// row a thread, in small blocks, since all that counts is that the loads of all
+// are under way at once.
+template <bool GATE>
+__global__ __launch_bounds__(64) void k_matmul_join(Args a)
+{
+    const uint32_t quads = (uint32_t)(a.units + 3) / 4;
+    const uint32_t i = blockIdx.x * 64 + threadIdx.x;
+    const int64_t row = i / quads;
+    if (row >= a.num_rows) return;
+    const int u = (int)(i % quads) * 4;
+    constexpr int G = GATE ? 2 : 1;
+    i32x4 sum[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) sum[g] = i32x4{0, 0, 0, 0};
+#pragma unroll 8
+    for (int s = 0; s < a.splits; ++s) {
+        const int32_t* const from = a.part + (s * a.num_rows + row) * a.rows + u;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if (a.vec) {
+                sum[g] += *reinterpret_cast<const i32x4*>(from + g * a.units);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (u + q < a.units) sum[g][q] += from[g * a.units + q];
+            }
+        }
+    }
+    const float x1 = a.x_scales[row];
+    uint16_t* const to = a.y + row * a.units + u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (u + q < a.units) {
+            float v = (float)sum[0][q] * x1 * a.w_scales[u + q];
+            if constexpr (GATE) v = v / (1.f + __expf(-v)) * ((float)sum[G - 1][q] * x1 * a.w_scales[a.units + u + q]);
+            to[q] = __builtin_bit_cast(uint16_t, (__bf16)v);
+        }
+}
+
 int num_cus()
 {
     static const int n = [] {
@@ -543,16 +630,26 @@ int64_t most_tiles(const Args& a, int64_t rows, int64_t bm)
     return n < rows ? n : rows;
 }
 
-template <int BM, int BN, int WM, int WN, int S, bool GATE>
+template <int BM, int BN, int WM, int WN, int S, bool GATE, bool SPLIT = false>
 hipError_t launch_tile(const Args& a, int64_t rows, hipStream_t s)
 {
     using T = Tile<BM, BN, WM, WN, S, GATE>;
-    const int64_t tiles = most_tiles(a, rows, BM) * ((a.units + T::kUnits - 1) / T::kUnits);
+    const int64_t tiles = most_tiles(a, rows, BM) * ((a.units + T::kUnits - 1) / T::kUnits) * (SPLIT ? a.splits : 1);
     const int64_t most = (int64_t)num_cus() / 8 * T::kBlocks, need = (tiles + 7) / 8;
     const dim3 grid((unsigned)(8 * (need < most ? need : most)));
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_matmul<BM, BN, WM, WN, S, GATE>),
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_matmul<BM, BN, WM, WN, S, GATE, SPLIT>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
-    hipLaunchKernelGGL((k_matmul<BM, BN, WM, WN, S, GATE>), grid, dim3(T::kThreads), (size_t)T::kLds, s, a);
+    hipLaunchKernelGGL((k_matmul<BM, BN, WM, WN, S, GATE, SPLIT>), grid, dim3(T::kThreads), (size_t)T::kLds, s, a);
+    return hipGetLastError();
+}
+
+template <bool GATE>
+hipError_t launch_split(const Args& a, int64_t rows, hipStream_t s)
+{
+    const hipError_t e = launch_tile<64, 64, 2, 2, stages(kPathTile64x64), GATE, true>(a, rows, s);
+    if (e != hipSuccess) return e;
+    const int64_t quads = rows * ((a.units + 3) / 4);      // at most 2^20 sums a split
+    hipLaunchKernelGGL((k_matmul_join<GATE>), dim3((unsigned)((quads + 63) / 64)), dim3(64), 0, s, a);
     return hipGetLastError();
 }
 
@@ -582,11 +679,18 @@ hipError_t launch_path(Path path, const Args& a, int64_t rows, hipStream_t s)
 }  // namespace
 }  // namespace mm
 
-hipError_t launch_matmul(const ProductArgs& p, bool gate, hipStream_t s)
+int64_t matmul_workspace(bool gate, int64_t cols, int64_t units, int64_t rows)
+{
+    const int n = mm::choose_splits(gate, cols, units, rows);
+    return n > 1 ? 4 * n * rows * units * (gate ? 2 : 1) : 0;
+}
+
+hipError_t launch_matmul(const ProductArgs& p, bool gate, int32_t* part, hipStream_t s)
 {
     const int64_t rows = p.count ? p.P : p.num_rows, cols = 2 * (int64_t)p.w.cols;
     const mm::Path path = mm::choose_path(gate, cols, p.units, p.count ? p.E : 0, rows);
     if (path == mm::kPathNone) return hipSuccess;
+    const int splits = part && !p.count ? mm::choose_splits(gate, cols, p.units, rows) : 1;
     if (path == mm::kPathFew) return launch_product_int8(p, gate ? kSwigluBf16 : kStoreBf16, s);
     mm::Args a = {};
     a.w = p.w.data;
@@ -604,6 +708,11 @@ hipError_t launch_matmul(const ProductArgs& p, bool gate, hipStream_t s)
     a.cap = p.cap;
     a.y = static_cast<uint16_t*>(p.y);
     a.flags = p.flags;
+    if (splits > 1) {
+        a.splits = splits;
+        a.part = part;
+        return gate ? mm::launch_split<true>(a, rows, s) : mm::launch_split<false>(a, rows, s);
+    }
     return gate ? mm::launch_path<true>(path, a, rows, s) : mm::launch_path<false>(path, a, rows, s);
 }
 

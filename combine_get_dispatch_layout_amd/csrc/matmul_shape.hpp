@@ -54,6 +54,12 @@ constexpr TileCost kTileCosts[] = {
     {kPathTile256, 256, 256, 256, 1.0f, 1.0f, 2.0f},
 };
 
+// Weight tiles of 16 rows for each 16 rows of x.
+inline int64_t thin_tiles(bool gate, int64_t units, int64_t rows)
+{
+    return (rows + 15) / 16 * ((units + 15) / 16) * (gate ? 2 : 1);
+}
+
 // cols, units of the weight matrix; experts: 0 for one matrix; rows: of all
 // experts.
 inline Path choose_path(bool gate, int64_t cols, int64_t units, int64_t experts, int64_t rows)
@@ -70,7 +76,7 @@ inline Path choose_path(bool gate, int64_t cols, int64_t units, int64_t experts,
     //   tiles    256             512             896
     //   thin     7.9-10 (4.5-5)  13-17 (6-7)     21-29 (10-13)
     //   64 x 64  20     (7.8)    21    (7.8)     22    (8.0)
-    if (!grouped && rows <= 32 && (rows + 15) / 16 * ((units + 15) / 16) * (gate ? 2 : 1) <= 640) return kPathThin;
+    if (!grouped && rows <= 32 && thin_tiles(gate, units, rows) <= 640) return kPathThin;
     // decode batches of many experts: 256 experts, 7168 -> 2048, 4, 8, 12 rows an
     // expert 554, 572, 668 us, with 64 x 128 tiles 610, 618, 626; 64 experts, 2048
     // -> 2 x 768, 8 and 12 rows 37, 42, with tiles 38, 39
@@ -95,6 +101,34 @@ inline Path choose_path(bool gate, int64_t cols, int64_t units, int64_t experts,
         }
     }
     return best;
+}
+
+// Tiles of 64 x 64 of one matrix are often fewer than CUs, and what bounds a block
+// alone is the way of its columns into LDS (a step 0.36 us, with any number of
+// stages); the thin kernel's blocks wait 2 us for each 4096 columns.  With a
+// workspace for the sums the columns are split over blocks, at most 256 in all
+// (4 MB of sums) and 32 for a tile, eight steps each at least, and a second kernel
+// joins them, which costs 6.5 us in all.  In us, alone and split in (n):
+//   64 rows   2048 -> 2048  8.6, 9.2 (4)     7168 -> 4096  22, 14 (4)
+//             16384 -> 4096  47, 21 (4)      18432 -> 7168  53, 35 (2)
+//   16 rows   32768 -> 1024  30, 17 (16)
+//   256 rows  4096 -> 4096 (256 tiles)  14.6, 17.5 (2)
+//   33 rows   131056 -> 64  345, split in 32, 64, 128: 28, 30, 41
+// The second launch also costs its caller some 4 us.
+inline int choose_splits(bool gate, int64_t cols, int64_t units, int64_t rows)
+{
+    const int64_t steps = (cols + kStep - 1) / kStep;
+    const int64_t tiles = (rows + 63) / 64 * (((gate ? 2 : 1) * units + 63) / 64);
+    if (tiles < 1 || tiles > 128) return 1;
+    int64_t n = 256 / tiles < steps / 8 ? 256 / tiles : steps / 8;
+    if (n > 32) n = 32;
+    if (n < 2) return 1;
+    float alone = 1.f + 0.36f * steps;
+    if (choose_path(gate, cols, units, 0, rows) == kPathThin) {
+        const float all = 3.f + (float)(thin_tiles(gate, units, rows) * 16 * cols) / 4.2e6f, wait = 4.f + cols / 2048.f;
+        alone = all > wait ? all : wait;
+    }
+    return alone > 11.f + 0.36f * ((steps + n - 1) / n) ? (int)n : 1;
 }
 
 }  // namespace mm

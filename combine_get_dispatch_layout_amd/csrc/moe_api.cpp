@@ -199,13 +199,19 @@ ep_status check_activation(const ep_weights* w, int32_t activation)
     return EP_OK;
 }
 
-ep_status check_rows(const ep_weights* w, const void* d_x, int64_t rows, const void* d_y)
+ep_status check_row_count(const ep_weights* w, int64_t rows)
 {
     // the kernels number (row, 16 outputs) tiles in 32 bits
     if (rows < 0 || rows >= (int64_t)1 << 31 || rows * ((w->rows + 15) / 16) >= (int64_t)1 << 31)
         return EP_FAIL(EP_ERR_INVALID_ARG, "%lld rows times %d outputs outside [0, 2^35)",
                        (long long)rows, w->rows);
-    if (rows == 0) return EP_OK;
+    return EP_OK;
+}
+
+ep_status check_rows(const ep_weights* w, const void* d_x, int64_t rows, const void* d_y)
+{
+    const ep_status st = check_row_count(w, rows);
+    if (st != EP_OK || rows == 0) return st;
     if (!d_x || !d_y) return EP_FAIL(EP_ERR_INVALID_ARG, "x or y is NULL");
     if (!aligned(d_x, 16) || !aligned(d_y, 2))
         return EP_FAIL(EP_ERR_INVALID_ARG, "x must be 16-byte aligned, y 2-byte aligned");
@@ -482,7 +488,42 @@ ep_status ep_matmul(const ep_weights* w, const void* d_x, const float* d_x_scale
     if (st == EP_OK) st = check_x_scales(d_x_scales, num_rows);
     if (st != EP_OK) return st;
     a.x_scales = d_x_scales;
-    EP_HIP(epk::launch_matmul(a, activation == EP_ACT_SWIGLU, static_cast<hipStream_t>(stream)));
+    EP_HIP(epk::launch_matmul(a, activation == EP_ACT_SWIGLU, nullptr, static_cast<hipStream_t>(stream)));
+    return EP_OK;
+}
+
+ep_status ep_matmul_workspace_size(const ep_weights* w, int64_t num_rows, int32_t activation, int64_t* bytes)
+{
+    ep_status st = check_weights(w, "w", false, true);
+    if (st == EP_OK) st = check_activation(w, activation);
+    if (st == EP_OK) st = check_row_count(w, num_rows);
+    if (st != EP_OK) return st;
+    if (w->num_experts != 1)
+        return EP_FAIL(EP_ERR_INVALID_ARG, "ep_matmul takes one matrix (num_experts=%d)", w->num_experts);
+    if (!bytes) return EP_FAIL(EP_ERR_INVALID_ARG, "bytes is NULL");
+    const bool gate = activation == EP_ACT_SWIGLU;
+    *bytes = epk::matmul_workspace(gate, w->cols, gate ? w->rows / 2 : w->rows, num_rows);
+    return EP_OK;
+}
+
+ep_status ep_matmul_split(const ep_weights* w, const void* d_x, const float* d_x_scales,
+                          int64_t num_rows, int32_t activation, void* d_y, void* d_workspace,
+                          int64_t workspace_bytes, void* stream)
+{
+    epk::ProductArgs a;
+    ep_status st = check_dense(w, true, d_x, num_rows, activation, d_y, &a);
+    if (st == EP_OK) st = check_x_scales(d_x_scales, num_rows);
+    if (st != EP_OK) return st;
+    const bool gate = activation == EP_ACT_SWIGLU;
+    const int64_t need = epk::matmul_workspace(gate, w->cols, a.units, num_rows);
+    if (need > 0 && (!d_workspace || !aligned(d_workspace, 256)))
+        return EP_FAIL(EP_ERR_WORKSPACE, "workspace must be 256-byte aligned and not NULL");
+    if (workspace_bytes < need)
+        return EP_FAIL(EP_ERR_WORKSPACE, "workspace has %lld bytes, needs %lld",
+                       (long long)workspace_bytes, (long long)need);
+    a.x_scales = d_x_scales;
+    EP_HIP(epk::launch_matmul(a, gate, need > 0 ? static_cast<int32_t*>(d_workspace) : nullptr,
+                              static_cast<hipStream_t>(stream)));
     return EP_OK;
 }
 
@@ -495,7 +536,7 @@ ep_status ep_expert_matmul(const ep_handle* h, const ep_weights* w, const void* 
     if (st == EP_OK) st = check_x_scales(d_x_scales, x_rows);
     if (st != EP_OK) return st;
     a.x_scales = d_x_scales;
-    EP_HIP(epk::launch_matmul(a, activation == EP_ACT_SWIGLU, static_cast<hipStream_t>(stream)));
+    EP_HIP(epk::launch_matmul(a, activation == EP_ACT_SWIGLU, nullptr, static_cast<hipStream_t>(stream)));
     return EP_OK;
 }
 

@@ -234,3 +234,8 @@ extern "C" int ep_probe_matmul_path(int gate, int64_t cols, int64_t units, int64
 {
     return epk::mm::choose_path(gate != 0, cols, units, experts, rows);
 }
+
+extern "C" int ep_probe_matmul_splits(int gate, int64_t cols, int64_t units, int64_t rows)
+{
+    return epk::mm::choose_splits(gate != 0, cols, units, rows);
+}

@@ -25,7 +25,7 @@ EP_BALANCE_MAX_SEQUENCES = 1 << 18
 # Every symbol include/ep_moe.h declares.
 SYMBOLS = ("ep_gate", "ep_gate_backward", "ep_balance_workspace_size", "ep_balance_loss",
            "ep_balance_loss_backward", "ep_matvec", "ep_expert_matvec", "ep_matmul",
-           "ep_expert_matmul", "ep_moe_workspace_size", "ep_moe_layer")
+           "ep_matmul_workspace_size", "ep_matmul_split", "ep_expert_matmul", "ep_moe_workspace_size", "ep_moe_layer")
 
 
 class ep_gate_config(ctypes.Structure):
@@ -64,6 +64,8 @@ def _lib():
         L.ep_balance_loss.argtypes = [P, P, P, P, I64, P, I64, P, P, P, P, P, I64, P]
         L.ep_balance_loss_backward.argtypes = [P, P, P, I64, P, I64, P, P, P, P, P]
         L.ep_matmul.argtypes = [P, P, P, I64, I32, P, P]
+        L.ep_matmul_workspace_size.argtypes = [P, I64, I32, P]
+        L.ep_matmul_split.argtypes = [P, P, P, I64, I32, P, P, I64, P]
         L.ep_expert_matmul.argtypes = [P, P, P, P, I64, I32, P, P]
         L.ep_moe_workspace_size.argtypes = [P, P, P, I64, P]
         L.ep_moe_layer.argtypes = [P, P, P, P, P, P, I64, P, P, I64, P]
@@ -417,6 +419,7 @@ class Weights:
         self.device = data.device
         self._c = ep_weights(format, group, E, M, C, 0, _ptr(data), _ptr(scales), _ptr(zeros))
         self._ref = ctypes.byref(self._c)
+        self._workspace = {}        # bytes for (rows, activation) of ep_matmul
 
 
 def _check_product(w, x, y, activation, dtype=torch.bfloat16):
@@ -462,14 +465,34 @@ def _check_x_scales(x, x_scales):
         _check_tensor("x_scales", x_scales, (torch.float32,), (x.shape[0],), x.device)
 
 
+def ep_matmul_workspace_size(w: Weights, rows: int, activation: int = EP_ACT_NONE) -> int:
+    n = w._workspace.get((rows, activation))
+    if n is None:
+        out = ctypes.c_int64()
+        _check(_lib().ep_matmul_workspace_size(w._ref, rows, activation, ctypes.byref(out)))
+        n = w._workspace[rows, activation] = out.value
+    return n
+
+
 def ep_matmul(w: Weights, x: torch.Tensor, x_scales: torch.Tensor, y: Optional[torch.Tensor] = None,
-              activation: int = EP_ACT_NONE):
+              activation: int = EP_ACT_NONE, workspace: Optional[torch.Tensor] = None):
     """y bf16 = act((x W^T) * x_scales * w's scales) in 8-bit integers, for x
     int8 [rows, cols] with x_scales fp32 [rows] or [rows, 1] and one matrix
-    (INT8 weights)."""
+    (INT8 weights).  Few rows of many columns are split (ep_matmul_split) in a
+    workspace: uint8, at least ep_matmul_workspace_size bytes (allocated for this
+    call when not given)."""
     y = _check_product(w, x, y, activation, torch.int8)
     _check_x_scales(x, x_scales)
-    _call(x.device, _lib().ep_matmul, w._ref, _ptr(x), _ptr(x_scales), x.shape[0], activation, _ptr(y))
+    need = ep_matmul_workspace_size(w, x.shape[0], activation)
+    if need == 0:
+        _call(x.device, _lib().ep_matmul, w._ref, _ptr(x), _ptr(x_scales), x.shape[0], activation, _ptr(y))
+        return y
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    elif workspace.dtype != torch.uint8 or workspace.device != x.device:
+        raise ValueError(f"workspace must be uint8 on {x.device}")
+    _call(x.device, _lib().ep_matmul_split, w._ref, _ptr(x), _ptr(x_scales), x.shape[0], activation,
+          _ptr(y), _ptr(workspace), workspace.numel())
     return y
 
 

@@ -11,7 +11,9 @@
  *                       ep_combine)
  *   ep_matmul,          the same in 8-bit integers on both sides, for any
  *   ep_expert_matmul    number of rows: rows as an int8 dispatch delivers
- *                       them, with a scale for each row and each output
+ *                       them, with a scale for each row and each output;
+ *                       ep_matmul_split, with a workspace, is faster for
+ *                       few rows of many columns
  *   ep_moe_layer        the whole expert layer for a few tokens, from
  *                       topk_idx to the combined output, without the shuffle
  *   ep_balance_loss     per-expert counts of a routing and the balance loss,
@@ -233,6 +235,20 @@ ep_status ep_expert_matvec(const ep_handle* h, const ep_weights* w, const void* 
  *   num_rows * M below 2^35. */
 ep_status ep_matmul(const ep_weights* w, const void* d_x, const float* d_x_scales,
                     int64_t num_rows, int32_t activation, void* d_y, void* stream);
+
+/* Bytes of device workspace with which ep_matmul_split serves a call of these
+ * sizes: at most 4 MB, 0 where it does as ep_matmul. */
+ep_status ep_matmul_workspace_size(const ep_weights* w, int64_t num_rows, int32_t activation,
+                                   int64_t* bytes);
+
+/* ep_matmul, to the same bits, with a workspace for the sums of products that have
+ * few rows and outputs and many columns: those are split over more blocks.
+ *   d_workspace: 256-byte aligned, at least ep_matmul_workspace_size bytes (NULL
+ *   if that is 0), needs no clearing; in use by one stream (or graph in flight)
+ *   at a time. */
+ep_status ep_matmul_split(const ep_weights* w, const void* d_x, const float* d_x_scales,
+                          int64_t num_rows, int32_t activation, void* d_y, void* d_workspace,
+                          int64_t workspace_bytes, void* stream);
 
 /* The same for received rows, each with its expert's matrix: rows, layout, flags
  * and states as ep_expert_matvec; the scales of rows that hold no token are not

@@ -87,6 +87,10 @@ enum {
 };
 int ep_probe_matmul_path(int gate, int64_t cols, int64_t units, int64_t experts, int64_t rows);
 
+/* Over how many blocks ep_matmul_split spreads a product's columns, in tiles of 64
+ * rows and 64 weight rows; 1: it does as ep_matmul. */
+int ep_probe_matmul_splits(int gate, int64_t cols, int64_t units, int64_t rows);
+
 #ifdef __cplusplus
 }
 #endif
