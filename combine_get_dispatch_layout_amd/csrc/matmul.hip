@@ -471,12 +471,14 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
 
 // ---- few rows and outputs of one matrix --------------------------------------------
 //
-// A block has 16 outputs (16 gate and 16 up rows) of up to 16 rows; its waves take
-// the lines of 128 columns in turn, U of them in flight each, straight from memory
-// to registers, and add their sums in LDS (exact, so in any order).  What bounds it
-// is latency: the 29 MB of 7168 -> 4096 are 115 KB for each CU, and what counts is
-// that all of them are asked for at once.  One row 7.9 us (15 us with the few-row
-// kernel, whose 32-output tiles leave half of the CUs idle), 16 rows 10.2 (14.6).
+// A block has G groups of 16 outputs (or 16 gate and 16 up rows) of up to 16 rows;
+// its waves take the lines of 128 columns in turn, U of them in flight each,
+// straight from memory to registers, and add their sums in LDS (exact, so in any
+// order).  What bounds it is latency: the 29 MB of 7168 -> 4096 are 115 KB for each
+// CU, and what counts is that all of them are asked for at once.  One row 8.3 us
+// (15 us with the few-row kernel, whose 32-output tiles leave half of the CUs
+// idle), 16 rows 10.4 (14.6).  Each block begins at lines of its own, as the tiles
+// above do: one row, 16384 -> 4096 14.4 us, all from line 0 18.2.
 //
 // A load of weights takes 8 rows x 128 bytes (whole cache lines); of two, lanes
 // 0-7 and 8-15 of each row of 16 lanes trade one, which makes two operands: lane
@@ -496,39 +498,43 @@ __device__ __forceinline__ u32x4 load_line(Buffer b, uint32_t lane_off, uint32_t
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_off, off, 0));
 }
 
-template <int U, bool GATE>
+template <int U, int G, bool GATE>
 __global__ __launch_bounds__(kThinWaves* kWave) void k_matmul_thin(Args a)
 {
-    constexpr int G = GATE ? 2 : 1;
+    static_assert(!GATE || G == 2, "a gate and an up group");
+    constexpr int NO = GATE ? 1 : G;        // groups of outputs
     __shared__ i32x4 sums[kThinWaves][G][kWave];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, c = lane >> 4;
-    const int unit0 = blockIdx.x * 16, have = min(16, a.units - unit0);
+    const int unit0 = blockIdx.x * 16 * NO;
     const int64_t row0 = (int64_t)blockIdx.y * 16;
     const int rows = (int)min((int64_t)16, a.num_rows - row0);
     Buffer wb[G];
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-        wb[g] = make_buffer(a.w + ((int64_t)g * a.units + unit0) * a.cols, (int64_t)have * a.cols);
+    for (int g = 0; g < G; ++g) {
+        const int u0 = GATE ? unit0 : min(unit0 + 16 * g, a.units), have = min(16, a.units - u0);
+        wb[g] = make_buffer(a.w + ((GATE ? (int64_t)g * a.units : 0) + u0) * a.cols, (int64_t)have * a.cols);
+    }
     const Buffer xb = make_buffer(a.x + row0 * a.cols, (int64_t)rows * a.cols);
     uint32_t wo[2];
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
         const int r = 8 * v + (lane & 7);
-        wo[v] = r < have ? (uint32_t)r * (uint32_t)a.cols + 16u * (lane >> 3) : kNowhere;
+        wo[v] = (uint32_t)r * (uint32_t)a.cols + 16u * (lane >> 3);     // (past the last row: past the buffer)
     }
     const uint32_t xo = (uint32_t)n * (uint32_t)a.cols + 32u * c;
 
     i32x4 acc[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) acc[g] = i32x4{0, 0, 0, 0};
-    const int lines = (a.cols + 127) / 128;
+    const int lines = (a.cols + 127) / 128, turn = (int)(blockIdx.x * 3u % (uint32_t)lines);
     for (int l0 = wave; l0 < lines; l0 += kThinWaves * U) {
         u32x4 w[U][G][2], x[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int line = l0 + u * kThinWaves, left = a.cols - line * 128;   // columns from it on
+            const int at = l0 + u * kThinWaves, line = at + turn < lines ? at + turn : at + turn - lines;
+            const int left = at < lines ? a.cols - line * 128 : 0;              // columns from it on
             const uint32_t off = left > 0 ? (uint32_t)line * 128u : 0u;
 #pragma unroll
             for (int g = 0; g < G; ++g)
@@ -552,20 +558,23 @@ __global__ __launch_bounds__(kThinWaves* kWave) void k_matmul_thin(Args a)
 #pragma unroll
     for (int g = 0; g < G; ++g) sums[wave][g][lane] = acc[g];
     __syncthreads();
-    // a lane of the first wave has outputs 4c to 4c + 3 of row n
-    const int u = unit0 + 4 * c;
-    if (wave != 0 || n >= rows || u >= a.units) return;
+    // a lane of the first waves has outputs 4c to 4c + 3 of row n, a group a wave
+    const int u = unit0 + 16 * wave + 4 * c;
+    if (wave >= NO || n >= rows || u >= a.units) return;
+    i32x4 sum[GATE ? 2 : 1];
+#pragma unroll
+    for (int g = 0; g < (GATE ? 2 : 1); ++g) {
+        sum[g] = i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kThinWaves; ++w) sum[g] += sums[w][GATE ? g : wave][lane];
+    }
     const float x1 = a.x_scales[row0 + n];
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int w = 1; w < kThinWaves; ++w) acc[g] += sums[w][g][lane];
     uint16_t* const to = a.y + (row0 + n) * a.units + u;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
         if (u + q < a.units) {
-            float v = (float)acc[0][q] * x1 * a.w_scales[u + q];
-            if constexpr (GATE) v = v / (1.f + __expf(-v)) * ((float)acc[1][q] * x1 * a.w_scales[a.units + u + q]);
+            float v = (float)sum[0][q] * x1 * a.w_scales[u + q];
+            if constexpr (GATE) v = v / (1.f + __expf(-v)) * ((float)sum[1][q] * x1 * a.w_scales[a.units + u + q]);
             to[q] = __builtin_bit_cast(uint16_t, (__bf16)v);
         }
 }
@@ -653,11 +662,12 @@ hipError_t launch_split(const Args& a, int64_t rows, hipStream_t s)
     return hipGetLastError();
 }
 
-template <int U, bool GATE>
+template <int U, int G, bool GATE>
 hipError_t launch_thin(const Args& a, int64_t rows, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.units + 15) / 16), (unsigned)((rows + 15) / 16));
-    hipLaunchKernelGGL((k_matmul_thin<U, GATE>), grid, dim3(kThinWaves * kWave), 0, s, a);
+    const int outputs = GATE ? 16 : 16 * G;
+    const dim3 grid((unsigned)((a.units + outputs - 1) / outputs), (unsigned)((rows + 15) / 16));
+    hipLaunchKernelGGL((k_matmul_thin<U, G, GATE>), grid, dim3(kThinWaves * kWave), 0, s, a);
     return hipGetLastError();
 }
 
@@ -667,8 +677,17 @@ hipError_t launch_path(Path path, const Args& a, int64_t rows, hipStream_t s)
     switch (path) {
         case kPathThin:
             // two lines a wave at once if that is all there are: 2048 columns 4.4 us
-            // (4.7 with four), 7168 columns 8.5 (7.9)
-            return a.cols <= 2 * kThinWaves * 128 ? launch_thin<2, GATE>(a, rows, s) : launch_thin<4, GATE>(a, rows, s);
+            // (4.7 with four), 7168 columns 8.5 (7.9).  Two groups of outputs a block,
+            // for one reading of x, where that makes about a block a CU: 16 rows, 18432
+            // -> 7168 (224 blocks) 30 us, one group 38; 4096 -> 8192 (256) 9.3 and 10.7;
+            // 4096 -> 4096 (128) 8.5 and 7.2, 7168 -> 8704 (272) 23.7 and 23.0, one row
+            // 20.3 and 17.3
+            if constexpr (!GATE)
+                if (const int64_t t = thin_tiles(false, a.units, rows); t >= 448 && t <= 512)
+                    return a.cols <= 2 * kThinWaves * 128 ? launch_thin<2, 2, false>(a, rows, s)
+                                                          : launch_thin<4, 2, false>(a, rows, s);
+            return a.cols <= 2 * kThinWaves * 128 ? launch_thin<2, GATE ? 2 : 1, GATE>(a, rows, s)
+                                                  : launch_thin<4, GATE ? 2 : 1, GATE>(a, rows, s);
         case kPathTile64x64: return launch_tile<64, 64, 2, 2, stages(kPathTile64x64), GATE>(a, rows, s);
         case kPathTile64x128: return launch_tile<64, 128, 1, 4, stages(kPathTile64x128), GATE>(a, rows, s);
         case kPathTile128: return launch_tile<128, 128, 2, 2, stages(kPathTile128), GATE>(a, rows, s);

@@ -73,9 +73,9 @@ inline Path choose_path(bool gate, int64_t cols, int64_t units, int64_t experts,
     const int64_t steps = (cols + kStep - 1) / kStep;
     // the thin kernel's time follows its weight tiles of 16, 64 x 64 tiles' hardly
     // does below 256: us with 7168 columns (and 2048), 1 to 16 rows:
-    //   tiles    256             512             896
-    //   thin     7.9-10 (4.5-5)  13-17 (6-7)     21-29 (10-13)
-    //   64 x 64  20     (7.8)    21    (7.8)     22    (8.0)
+    //   tiles    256             512             640             896
+    //   thin     8.3-10 (4.5-5)  13-14 (6-7)     18-23 (7-9)     21-26 (9-10)
+    //   64 x 64  21     (7.8)    21    (7.8)     22    (8.6)     22    (9.0)
     if (!grouped && rows <= 32 && thin_tiles(gate, units, rows) <= 640) return kPathThin;
     // decode batches of many experts: 256 experts, 7168 -> 2048, 4, 8, 12 rows an
     // expert 554, 572, 668 us, with 64 x 128 tiles 610, 618, 626; 64 experts, 2048

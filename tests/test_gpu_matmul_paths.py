@@ -132,6 +132,24 @@ def test_received_rows(path, N, E, K, C, M, act, align, cap, mask, skew):
             check(y[r], x[r], xs[r], w[e], s[e], act)
 
 
+@pytest.mark.parametrize("n,C,M", [(1, 7168, 7170), (5, 528, 8000), (16, 2064, 8191), (20, 1040, 3585), (32, 4112, 3599),
+                                   (17, 16, 4090), (2, 7184, 8177)])
+def test_thin_blocks_of_two_groups(n, C, M):
+    """448 to 512 weight tiles of 16 for 16 rows: two to a block, of which the
+    last one's second may be short or missing."""
+    say(f"[matmul thin pairs] {n} {C} {M}")
+    assert P.matmul(n, C, M) == P.THIN and P.splits(n, C, M) == 1
+    assert 448 <= (n + 15) // 16 * ((M + 15) // 16) <= 512
+    g = gen(n + M)
+    w, s, W = stack(g, 1, M, C)
+    x, xs = rows_of(g, n, C)
+    buf = torch.full((n * M + 8,), 77.0, dtype=torch.bfloat16, device="cuda")
+    y = buf[4:4 + n * M].view(n, M)
+    moe.ep_matmul(W, x, xs, y)
+    check(y, x, xs, w[0], s[0], 0)
+    assert (buf[:4] == 77).all() and (buf[4 + n * M:] == 77).all()
+
+
 @pytest.mark.parametrize("path,n,C,M", [(P.THIN, 20, 7168, 4096), (P.TILE64X64, 300, 1040, 520), (P.TILE64X128, 1024, 640, 4096),
                                         (P.TILE128, 2100, 272, 2050), (P.TILE256, 4096, 400, 4096)])
 def test_replays_and_streams(path, n, C, M):
