@@ -6,8 +6,12 @@
 //   S[q,e] = sum over t in V_q of p[t,e]
 //   loss   = coefficient / Q * sum_q E / (K T_q^2) * sum_e count[q,e] S[q,e]
 //
-// What bounds it: one reading of the logits (the gradient: and one writing),
-// for small batches the launches.
+// What bounds it: one reading of the logits (the gradient: and one writing) and
+// some 17 instructions a score, two of them at a quarter of the rate, which take as
+// long; for small batches the launches.  65536 tokens of 256 experts, fp32, sigmoid
+// scores in 37 sequences: 18 us and 9 for the second kernel, 27 in all (the bytes
+// at the rate of a large read: 9.6); the gradient 34 (the bytes at the rate of a
+// copy: 29).  4096 tokens of 128 experts, bf16: 3.8, 6.7 and 4.1 us.
 //
 // A token's experts lie in 16 lanes (64 above 256 experts), sixteen or fewer to
 // a lane: a reduction over them is four steps inside a row of lanes, for four

@@ -28,19 +28,23 @@
 // contiguous share of all tiles each, four tiles of rows by the tiles of outputs.
 //
 // Sums of integers may be taken in any order, so tiles of experts, or of one matrix
-// and few rows, begin at a step of their own and go round: blocks that start together would ask for the same
-// columns of rows a power of two apart, which lie in the same few channels of the
-// memory.  Where an expert has one tile of rows nothing is shared, and the tiles
-// of its outputs spread over all columns; with more, over four steps, so that they
-// still find each other's columns in L2.  128 experts of 45 rows, 4096 -> 1408:
+// and few rows, begin at a step of their own and go round: blocks that start
+// together would ask for the same columns of rows a power of two apart, which lie
+// in the same few channels of the memory.  Where an expert has one tile of rows
+// nothing is shared, and the tiles of its outputs spread over all columns; with
+// more, over four steps, so that they still find each other's columns in L2.  128 experts of 45 rows, 4096 -> 1408:
 // 144 us, all from column 0 154 to 160; 64 of 768, 1536 -> 4096: 368 and 382;
 // 128 of 256, 2048 -> 2 x 768: 168 and 171; 7168 columns: equal to 1 % slower.
 //
 // Where tiles are fewer than CUs, their columns are split over blocks if the caller
 // has room for the sums, which a second kernel joins (choose_splits).
 //
-// What bounds it: power, and behind that the way through LDS.  4096 rows, 7168 ->
-// 4096 run at 1.8 GHz of 2.4.
+// What bounds it.  One matrix: power, and behind that the way through LDS; 4096
+// rows, 7168 -> 4096, 96 to 105 us at 1.8 to 2.1 GHz of 2.4, 2.3 to 2.5 POP/s (the
+// library's plain products: 2.1 to 2.2).  Experts: the way of their columns from L2
+// to LDS, some 16 TB/s over the chip, and of the outputs to memory, which all CUs
+// write at once: 64 experts of 768 rows, 1536 -> 4096, 375 us, without the stores
+// 305, loads alone 257.
 #include "experts.hpp"
 #include "matmul_shape.hpp"
 
