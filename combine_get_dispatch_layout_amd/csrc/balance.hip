@@ -44,14 +44,14 @@ constexpr int kSmallWaves = 16, kSmallExperts = 256, kSmallTokens = 256, kSmallS
 
 constexpr float kLow = -__builtin_huge_valf();
 
-// exp(x) for |x| <= 150, off by an ulp or two: the rounding of x log2(e), which
-// the hardware's exp2 would magnify, is put right to first order.
+// exp(x) for |x| <= 150, off by an ulp or two: what the roundings of x log2(e) and
+// of that constant leave of x, which the hardware's exp2 would magnify (65 units of
+// 2^-24 at 87), is put right to first order, with log(2) in two parts.
 __device__ __forceinline__ float exp_near(float x)
 {
-    constexpr float kLog2E = 1.44269502f;
-    const float y = x * kLog2E;
+    const float y = x * 1.44269502f;
     const float r = __builtin_amdgcn_exp2f(y);
-    return fmaf(r, fmaf(x, kLog2E, -y) * 0.693147181f, r);
+    return fmaf(r, fmaf(-y, -1.90465421e-9f, fmaf(-y, 0.693147182f, x)), r);
 }
 
 __device__ __forceinline__ float reciprocal(float d)

@@ -116,6 +116,21 @@ def test_odd_logits(score, normalize):
     check(z, idx, None, np.array([0, 1, 2, 20, 48], np.int32), score, normalize)
 
 
+def test_scores_far_from_zero():
+    """A sigmoid alone, one token a sequence, so that score_sums holds it: 8 u at
+    every magnitude (balance_reference: the exponential 4, the sum 1, the
+    reciprocal 3), also where a rounded exponent would be off by 60."""
+    z = np.linspace(-87, 87, 1000 * 40, dtype=np.float32)
+    np.random.default_rng(2).shuffle(z)
+    z = z.reshape(1000, 40)
+    start = np.arange(1001, dtype=np.int32)
+    out = moe.ep_balance_loss(moe.BalanceConfig(40, 1, moe.EP_SCORE_SIGMOID, False), cu(z),
+                              cu(np.zeros((1000, 1), np.int32)), None, cu(start))
+    want = 1 / (1 + np.exp(-z.astype(np.float64)))
+    err = np.abs(out.score_sums.double().cpu().numpy() - want) / want
+    assert err.max() <= 8 * B.U, err.max() / B.U
+
+
 def test_nothing_left():
     """No token, all masked, no live entry, an expert that all take."""
     cfg = moe.BalanceConfig(24, 3, coefficient=2.0)
