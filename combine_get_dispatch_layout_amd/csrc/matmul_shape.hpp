@@ -79,8 +79,10 @@ inline Path choose_path(bool gate, int64_t cols, int64_t units, int64_t experts,
     if (!grouped && rows <= 32 && thin_tiles(gate, units, rows) <= 640) return kPathThin;
     // decode batches of many experts: 256 experts, 7168 -> 2048, 4, 8, 12 rows an
     // expert 554, 572, 668 us, with 64 x 128 tiles 610, 618, 626; 64 experts, 2048
-    // -> 2 x 768, 8 and 12 rows 37, 42, with tiles 38, 39
-    if (grouped && likely <= 8 && experts * ((outputs + 127) / 128) >= 512) return kPathFew;
+    // -> 2 x 768, 8 and 12 rows 37, 42, with tiles 38, 39.  Of few experts that have
+    // rows the tiles are faster: one row each of 48, 2048 -> 2 x 768 32 us and 36, of
+    // 32, 4096 -> 2 x 1408 68 and 82, of 128, 2048 -> 2 x 768 73 and 67
+    if (grouped && likely <= 8 && experts * ((outputs + 127) / 128) >= 1024) return kPathFew;
     Path best = kPathFew;
     float least = 0.f;
     for (const TileCost& t : kTileCosts) {
