@@ -58,12 +58,16 @@ namespace {
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+// Vectors at any address of their elements, so that rows of odd length are stored
+// as others are: 3324 rows, 1024 -> 2335, 18.6 us, element by element 25.6.
+typedef u32x4 Any16 __attribute__((aligned(2)));
+typedef u32x2 Any8 __attribute__((aligned(2)));
+typedef i32x4 AnySums __attribute__((aligned(4)));
 
 struct Args {
     const uint8_t* w;           // [E, rows, cols]
     const float* w_scales;      // [E, rows]
     int rows, cols, units;
-    bool vec;                   // rows of y take vectors of eight
     const uint8_t* x;           // [.., cols]
     const float* x_scales;
     int64_t num_rows;
@@ -396,8 +400,8 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
                     const int g = wn * NT + j;
                     const int u = p.unit0 + (GATE ? g / 2 : g) * 16 + 4 * c;
                     int32_t* const at4 = to + u + (GATE && g % 2 ? a.units : 0);
-                    if (a.vec) {
-                        if (u < a.units) *reinterpret_cast<i32x4*>(at4) = acc[i][j];
+                    if (u + 4 <= a.units) {
+                        *reinterpret_cast<AnySums*>(at4) = acc[i][j];
                     } else {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
@@ -436,28 +440,31 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
                     hi[o] = d[1];
                 }
                 uint16_t* const to = a.y + (p.row0 + m) * a.units;
-                if (a.vec) {
-                    // two groups: their lanes trade, 8 outputs of one group each
+                // two groups: their lanes trade, 8 outputs of one group each
 #pragma unroll
-                    for (int o = 0; o + 1 < NO; o += 2) {
-                        swap16(lo[o], lo[o + 1]);
-                        swap16(hi[o], hi[o + 1]);
-                        const int u = u0 + (o + c % 2) * 16 + c / 2 * 8;
-                        if (m < p.rows && u < a.units)
-                            *reinterpret_cast<u32x4*>(to + u) = u32x4{lo[o], hi[o], lo[o + 1], hi[o + 1]};
+                for (int o = 0; o + 1 < NO; o += 2) {
+                    swap16(lo[o], lo[o + 1]);
+                    swap16(hi[o], hi[o + 1]);
+                    const int u = u0 + (o + c % 2) * 16 + c / 2 * 8;
+                    const u32x4 d = {lo[o], hi[o], lo[o + 1], hi[o + 1]};
+                    if (m < p.rows && u + 8 <= a.units) {
+                        *reinterpret_cast<Any16*>(to + u) = d;
+                    } else if (m < p.rows) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (u + q < a.units) to[u + q] = (uint16_t)(d[q / 2] >> (q % 2 * 16));
                     }
-                    if constexpr (NO % 2 != 0) {
-                        const int u = u0 + (NO - 1) * 16 + 4 * c;
-                        if (m < p.rows && u < a.units) *reinterpret_cast<u32x2*>(to + u) = u32x2{lo[NO - 1], hi[NO - 1]};
+                }
+                if constexpr (NO % 2 != 0) {
+                    const int u = u0 + (NO - 1) * 16 + 4 * c;
+                    const u32x2 d = {lo[NO - 1], hi[NO - 1]};
+                    if (m < p.rows && u + 4 <= a.units) {
+                        *reinterpret_cast<Any8*>(to + u) = d;
+                    } else if (m < p.rows) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (u + q < a.units) to[u + q] = (uint16_t)(d[q / 2] >> (q % 2 * 16));
                     }
-                } else if (m < p.rows) {
-#pragma unroll
-                    for (int o = 0; o < NO; ++o)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int u = u0 + o * 16 + 4 * c + q;
-                            if (u < a.units) to[u] = (uint16_t)((q < 2 ? lo[o] : hi[o]) >> (q % 2 * 16));
-                        }
                 }
             }
         }
@@ -603,8 +610,8 @@ __global__ __launch_bounds__(64) void k_matmul_join(Args a)
         const int32_t* const from = a.part + (s * a.num_rows + row) * a.rows + u;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if (a.vec) {
-                sum[g] += *reinterpret_cast<const i32x4*>(from + g * a.units);
+            if (u + 4 <= a.units) {
+                sum[g] += *reinterpret_cast<const AnySums*>(from + g * a.units);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -721,7 +728,6 @@ hipError_t launch_matmul(const ProductArgs& p, bool gate, int32_t* part, hipStre
     a.rows = p.w.rows;
     a.cols = (int)cols;
     a.units = p.units;
-    a.vec = p.units % 8 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
     a.x = reinterpret_cast<const uint8_t*>(p.x);
     a.x_scales = p.x_scales;
     a.num_rows = p.num_rows;
