@@ -83,6 +83,10 @@ inline Path choose_path(bool gate, int64_t cols, int64_t units, int64_t experts,
     // rows the tiles are faster: one row each of 48, 2048 -> 2 x 768 32 us and 36, of
     // 32, 4096 -> 2 x 1408 68 and 82, of 128, 2048 -> 2 x 768 73 and 67
     if (grouped && likely <= 8 && experts * ((outputs + 127) / 128) >= 1024) return kPathFew;
+    // and of few tiles and many columns those kernels are faster, whose waves share
+    // the columns: 8 experts of 1 to 8 rows, 4096 -> 67 10 us, with 64 x 64 tiles 15;
+    // 7168 -> 2 x 512 18 and 23; 16 rows 27 and 24; 2560 -> 1024 11.1 and 10.8
+    if (grouped && likely <= 8 && experts * ((outputs + 31) / 32) <= 256 && steps >= 24) return kPathFew;
     Path best = kPathFew;
     float least = 0.f;
     for (const TileCost& t : kTileCosts) {

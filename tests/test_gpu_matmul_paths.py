@@ -81,6 +81,7 @@ def test_one_matrix(path, n, C, M, act):
 RECEIVED = [
     (P.FEW, 100, 64, 3, 272, 9000, 0, 1, 0, 0.1, 1.0),
     (P.FEW, 300, 30, 4, 128, 70, 1, 5, 0, 0.1, 1.0),
+    (P.FEW, 20, 8, 2, 4112, 66, 0, 1, 0, 0.1, 1.0), (P.FEW, 13, 9, 3, 7168, 514, 1, 8, 0, 0.0, 1.0),
     (P.TILE64X64, 250, 6, 2, 656, 130, 0, 1, 0, 0.1, 1.0),
     (P.TILE64X64, 90, 8, 4, 528, 258, 1, 16, 0, 0.0, 0.5),
     (P.TILE64X64, 60, 1024, 1, 656, 200, 0, 1, 0, 0.0, 0.0),
