@@ -120,7 +120,10 @@ struct Tile {
     static constexpr int kStageBytes = (BM + BN) * kStep;
     static constexpr int kUnits = GATE ? BN / 2 : BN;
     static constexpr int kScaleBytes = (BM + BN) * 4, kScaleLoads = (BM + BN) / 64;
-    static constexpr int kLds = S * kStageBytes + 2 * kScaleBytes;
+    // Tiles whose scales are held: a tile's are loaded when the last columns of the
+    // one before it have been, S - 1 steps ahead of the arithmetic.
+    static constexpr int kScales = scale_buffers(S);
+    static constexpr int kLds = S * kStageBytes + kScales * kScaleBytes;
     // blocks of a CU: 160 KB of LDS, 5 KB of which are static
     static constexpr int kBlocks = 163840 / (kLds + 5632);
     static_assert(BM % (kLoadRows * kWaves) == 0 && BN % (kLoadRows * kWaves) == 0, "whole loads");
@@ -272,7 +275,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
     const int last_cols = a.cols - (steps - 1) * kStep;         // of the last step
     uint32_t xo[T::kXLoads], wo[T::kWLoads];
     Buffer xb, wb;
-    int l_step = 0, l_k = 0, l_first = 0, l_steps = 0, l_parity = 0;
+    int l_step = 0, l_k = 0, l_first = 0, l_steps = 0, l_scales = 0;
     uint32_t l_tile = at;
     unsigned char* const scales = smem + S * T::kStageBytes;
     auto aim = [&] {
@@ -298,7 +301,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
             const Buffer xs = make_buffer(a.x_scales + p.row0, 4 * (int64_t)p.rows);
             const Buffer ws = make_buffer(a.w_scales + (int64_t)p.expert * a.rows, 4 * (int64_t)a.rows);
             for (int q = wave; q < T::kScaleLoads; q += T::kWaves) {
-                unsigned char* const to = scales + l_parity * T::kScaleBytes + q * 256;
+                unsigned char* const to = scales + l_scales * T::kScaleBytes + q * 256;
                 if (q < BM / 64) {
                     load_word_to_lds(xs, to, (uint32_t)(q * 64 + lane) * 4);
                 } else {
@@ -307,7 +310,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
                     load_word_to_lds(ws, to, u < a.units ? (uint32_t)(u + (GATE && r / 16 % 2 ? a.units : 0)) * 4 : kNowhere);
                 }
             }
-            l_parity ^= 1;
+            l_scales = l_scales == T::kScales - 1 ? 0 : l_scales + 1;
         }
         // Where a tile's columns begin.  (One matrix of many rows: at 0, where blocks
         // side by side share what they read; 4096 rows, 7168 -> 4096 102 us, turned
@@ -353,7 +356,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
     for (int s = 0; s < S - 1; ++s) load_stage(s);
     Where p;
     find(at, p);
-    int live = (p.rows + 15) / 16, parity = 0;      // groups of rows; scales
+    int live = (p.rows + 15) / 16, scale_buf = 0;   // groups of rows; scales
     i32x4 acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -412,9 +415,9 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
         } else {
             // ---- store: this lane has outputs 4c .. 4c+3 of row n of each group
             constexpr int NO = GATE ? NT / 2 : NT;      // groups of outputs
-            const float* const xs = reinterpret_cast<const float*>(scales + parity * T::kScaleBytes) + n;
+            const float* const xs = reinterpret_cast<const float*>(scales + scale_buf * T::kScaleBytes) + n;
             const f32x4* const ws =
-                reinterpret_cast<const f32x4*>(scales + parity * T::kScaleBytes + 4 * BM) + wn * NT * 4 + c;
+                reinterpret_cast<const f32x4*>(scales + scale_buf * T::kScaleBytes + 4 * BM) + wn * NT * 4 + c;
             f32x4 w4[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) w4[j] = ws[j * 4];
@@ -474,7 +477,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
             for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
         at += stride;
         if (at >= stop) return;
-        parity ^= 1;
+        scale_buf = scale_buf == T::kScales - 1 ? 0 : scale_buf + 1;
         find(at, p);
         live = (p.rows + 15) / 16;
     }

@@ -20,10 +20,13 @@ enum Path {
     kPathTile256 = 6        // 256 x 256
 };
 
-// Buffers of columns on their way (stages) of the tiled kernels.  They hold the
-// scales of two tiles, so a tile has to have more steps than stages, lest those of
-// a third be on their way.
+// Buffers of columns on their way (stages) of the tiled kernels, and of tiles'
+// scales.  Loads run S - 1 steps ahead of the arithmetic, a tile's scales are loaded
+// behind the last columns of the tile before; with B buffers they overwrite those
+// of B tiles before, whose arithmetic is then over if (B - 1) * steps > S - 1.
 constexpr int stages(Path p) { return p == kPathTile64x64 ? 4 : p == kPathTile64x128 ? 3 : 2; }
+constexpr int scale_buffers(int S) { return S == 2 ? 3 : 2; }
+constexpr bool enough_steps(Path p, int64_t steps) { return (scale_buffers(stages(p)) - 1) * steps > stages(p) - 1; }
 
 // The tiled kernels' time, in steps of a 256 x 256 tile (1.8 us): a step of a
 // round of tiles (one or two blocks to each CU) and what a round costs beside its
@@ -87,10 +90,12 @@ inline Path choose_path(bool gate, int64_t cols, int64_t units, int64_t experts,
     // the columns: 8 experts of 1 to 8 rows, 4096 -> 67 10 us, with 64 x 64 tiles 15;
     // 7168 -> 2 x 512 18 and 23; 16 rows 27 and 24; 2560 -> 1024 11.1 and 10.8
     if (grouped && likely <= 8 && experts * ((outputs + 31) / 32) <= 256 && steps >= 24) return kPathFew;
-    Path best = kPathFew;
+    // (two-stage tiles take any number of columns: 4096 rows, 256 -> 4096 13 us, the
+    // few-row kernels 37; 128 experts of 64 rows, 256 -> 2048 31 and 55)
+    Path best = kPathNone;
     float least = 0.f;
     for (const TileCost& t : kTileCosts) {
-        if (steps <= stages(t.path)) continue;
+        if (!enough_steps(t.path, steps)) continue;
         // an expert's tiles of rows: experts differ, so half a tile more where the
         // mean is near a whole number of them
         const float tiles_m = !grouped ? (float)((likely + t.bm - 1) / t.bm)
@@ -101,7 +106,7 @@ inline Path choose_path(bool gate, int64_t cols, int64_t units, int64_t experts,
         // half of a step's cost goes with the weights, half with the rows there are
         const float step = whole * t.step + (rest == 0 ? 0.f : rest <= 256 ? t.alone : t.step);
         const float cost = step * (0.5f + 0.5f * fill) * steps + (whole + (rest > 0 ? 1 : 0)) * t.round;
-        if (best == kPathFew || cost < least) {
+        if (best == kPathNone || cost < least) {
             best = t.path;
             least = cost;
         }

@@ -51,12 +51,15 @@ def check(y, x, xs, w, s, act):
 DENSE = [
     (P.THIN, 1, 16, 1, 0), (P.THIN, 3, 2048, 38, 0), (P.THIN, 5, 4112, 70, 0), (P.THIN, 16, 2064, 34, 1),
     (P.THIN, 17, 400, 34, 1), (P.THIN, 32, 2064, 514, 0), (P.THIN, 31, 7184, 4098, 0),
-    (P.FEW, 40, 256, 300, 0), (P.FEW, 1000, 128, 66, 1), (P.FEW, 3000, 16, 2050, 0),
+    (P.TILE128, 40, 256, 300, 0), (P.TILE128, 1000, 128, 66, 1), (P.TILE128, 3000, 16, 2050, 0),
+    (P.TILE128, 9000, 144, 4098, 0), (P.TILE128, 9001, 112, 4100, 1), (P.TILE128, 30000, 256, 2050, 0),
+    (P.TILE128, 30000, 128, 2050, 0), (P.TILE128, 30001, 48, 2062, 1), (P.TILE64X128, 700, 384, 2050, 0),
+    (P.TILE64X64, 300, 512, 2050, 0),
     (P.TILE64X64, 33, 528, 130, 0), (P.TILE64X64, 65, 656, 66, 1), (P.TILE64X64, 300, 1040, 520, 0),
     (P.TILE64X64, 1, 2048, 20000, 0), (P.TILE64X64, 127, 528, 1, 0), (P.TILE64X64, 700, 2048, 2, 1),
     (P.TILE64X128, 1500, 528, 2050, 0), (P.TILE64X128, 1500, 528, 1500, 1), (P.TILE64X128, 1024, 640, 4096, 0),
     (P.TILE64X128, 900, 528, 4000, 1),
-    (P.TILE128, 33, 272, 4000, 0), (P.TILE128, 2100, 272, 2050, 0), (P.TILE128, 2300, 384, 2062, 1),
+    (P.TILE64X128, 33, 272, 4000, 0), (P.TILE128, 2100, 272, 2050, 0), (P.TILE128, 2300, 384, 2062, 1),
     (P.TILE128, 3000, 528, 3002, 0), (P.TILE128, 4100, 400, 4110, 1),
     (P.TILE256, 3800, 272, 3900, 0), (P.TILE256, 3700, 272, 4000, 1), (P.TILE256, 4096, 400, 4096, 0),
     (P.TILE256, 4096, 1024, 4096, 1), (P.TILE256, 7900, 384, 3841, 0),
@@ -80,7 +83,11 @@ def test_one_matrix(path, n, C, M, act):
 # capacity, share of masked entries, skew
 RECEIVED = [
     (P.FEW, 100, 64, 3, 272, 9000, 0, 1, 0, 0.1, 1.0),
-    (P.FEW, 300, 30, 4, 128, 70, 1, 5, 0, 0.1, 1.0),
+    (P.TILE128, 300, 30, 4, 128, 70, 1, 5, 0, 0.1, 1.0), (P.TILE128, 20000, 30, 4, 256, 700, 1, 5, 0, 0.1, 1.0),
+    (P.TILE64X64, 3000, 200, 2, 512, 258, 0, 1, 0, 0.1, 0.5), (P.TILE64X128, 3000, 200, 2, 384, 514, 1, 1, 0, 0.1, 0.5),
+    (P.TILE64X128, 3000, 200, 2, 384, 1026, 0, 1, 0, 0.1, 0.5),
+    (P.TILE128, 6000, 128, 4, 128, 1026, 0, 1, 0, 0.1, 1.0), (P.TILE128, 30000, 4, 2, 256, 2000, 0, 1, 0, 0.0, 0.02),
+    (P.TILE128, 30000, 4, 2, 16, 2000, 0, 1, 0, 0.0, 0.02),
     (P.FEW, 20, 8, 2, 4112, 66, 0, 1, 0, 0.1, 1.0), (P.FEW, 13, 9, 3, 7168, 514, 1, 8, 0, 0.0, 1.0),
     (P.TILE64X64, 250, 6, 2, 656, 130, 0, 1, 0, 0.1, 1.0),
     (P.TILE64X64, 90, 8, 4, 528, 258, 1, 16, 0, 0.0, 0.5),
@@ -185,7 +192,9 @@ def test_replays_and_streams(path, n, C, M):
 
 
 @pytest.mark.parametrize("path,n,C,M", [(P.TILE64X64, 300, 1040, 520), (P.TILE64X128, 1024, 640, 4096),
-                                        (P.TILE128, 2100, 272, 2048), (P.TILE256, 4096, 400, 4096)])
+                                        (P.TILE128, 2100, 272, 2048), (P.TILE256, 4096, 400, 4096),
+                                        (P.TILE64X64, 20000, 512, 130), (P.TILE128, 20000, 256, 2048),
+                                        (P.TILE128, 20000, 128, 2048)])
 def test_scales_follow_their_tiles(path, n, C, M):
     """Tiles in a row on one block: scales that differ by powers of two from row
     to row and output to output would show another tile's."""

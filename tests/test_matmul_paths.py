@@ -6,8 +6,12 @@ import pytest
 
 import matmul_paths as P
 
-# (path, stages): a tile has to have more steps of 128 columns than stages
+# (path, stages): loads run stages - 1 steps of 128 columns ahead, and a tile's
+# scales are loaded behind the last columns of the tile before, stages steps before
+# its first.  They overwrite those of the tile `buffers` before, whose last step is
+# (buffers - 1) * steps before that first one: not sooner than its end with
 STAGES = {P.TILE64X64: 4, P.TILE64X128: 3, P.TILE128: 2, P.TILE256: 2}
+BUFFERS = {P.TILE64X64: 2, P.TILE64X128: 2, P.TILE128: 3, P.TILE256: 3}
 
 
 def test_nothing_and_little():
@@ -20,14 +24,14 @@ def test_nothing_and_little():
     assert P.matmul(65536, 7168, 4096, act=1, experts=256) == P.TILE256
 
 
-def test_short_rows_have_no_tiles():
-    """Up to two steps no tiled kernel is right; with three or four only those of
-    fewer stages."""
+def test_short_rows():
+    """With one or two steps only tiles of two stages and three buffers of scales
+    are right, with three also those of three stages."""
     rng = random.Random(3)
     for _ in range(3000):
         cols = 16 * rng.randint(1, 48)
         p = P.matmul(rng.randint(1, 20000), cols, 2 * rng.randint(1, 5000), rng.randint(0, 1), rng.choice([0, 1, 4, 64, 1024]))
-        assert p != P.NONE and (p not in STAGES or (cols + 127) // 128 > STAGES[p]), (cols, p)
+        assert p != P.NONE and (p not in STAGES or (BUFFERS[p] - 1) * ((cols + 127) // 128) >= STAGES[p]), (cols, p)
 
 
 def test_thin_is_for_one_matrix():
