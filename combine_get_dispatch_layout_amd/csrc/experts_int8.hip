@@ -1,5 +1,5 @@
-// Products of int8 rows with int8 weights: the kernels of product.hpp for this
-// format.
+// Products of few int8 rows an expert with int8 weights: the kernels of product.hpp
+// for this format.
 #include "product.hpp"
 
 namespace epk {

@@ -1232,7 +1232,10 @@ hipError_t launch_kind(const ProductArgs& a, hipStream_t s)
         case kPathSmall: return launch_shape<KIND, EPI, 1, false, kSpansSmall, 4>(a, c, rows, s);
         case kPathOneTile: return launch_shape<KIND, EPI, 1, false, spans_ahead(KIND, false), 8>(a, c, rows, s);
         case kPathMemory: return launch_shape<KIND, EPI, 1, true, spans_ahead(KIND, true), 8>(a, c, rows, s);
-        default: return launch_shape<KIND, EPI, 2, false, spans_ahead(KIND, false), two_tile_waves(KIND)>(a, c, rows, s);
+        default:
+            // (int8 rows above 8 an expert go to the tiled kernels)
+            if constexpr (KIND == kInt8) return hipErrorInvalidValue;
+            else return launch_shape<KIND, EPI, 2, false, spans_ahead(KIND, false), two_tile_waves(KIND)>(a, c, rows, s);
     }
 }
 
