@@ -100,8 +100,6 @@ __device__ __forceinline__ void load_word_to_lds(Buffer b, unsigned char* to, ui
     __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)to, 4, lane_off, 0, 0, 0);
 }
 
-constexpr uint32_t kNowhere = 0x80000000u;      // past every buffer: reads 0
-
 __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b)
 {
     const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
@@ -527,16 +525,10 @@ __global__ __launch_bounds__(kThinWaves* kWave) void k_matmul_thin(Args a)
     Buffer wb[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const int u0 = GATE ? unit0 : min(unit0 + 16 * g, a.units), have = min(16, a.units - u0);
-        wb[g] = make_buffer(a.w + ((GATE ? (int64_t)g * a.units : 0) + u0) * a.cols, (int64_t)have * a.cols);
+        const ThinGroup at = thin_group(unit0, GATE ? 0 : g, a.units);
+        wb[g] = make_buffer(a.w + ((GATE ? (int64_t)g * a.units : 0) + at.first) * a.cols, (int64_t)at.have * a.cols);
     }
     const Buffer xb = make_buffer(a.x + row0 * a.cols, (int64_t)rows * a.cols);
-    uint32_t wo[2];
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-        const int r = 8 * v + (lane & 7);
-        wo[v] = (uint32_t)r * (uint32_t)a.cols + 16u * (lane >> 3);     // (past the last row: past the buffer)
-    }
     const uint32_t xo = (uint32_t)n * (uint32_t)a.cols + 32u * c;
 
     i32x4 acc[G];
@@ -553,7 +545,8 @@ __global__ __launch_bounds__(kThinWaves* kWave) void k_matmul_thin(Args a)
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int v = 0; v < 2; ++v) w[u][g][v] = load_line(wb[g], 16 * (lane >> 3) < left ? wo[v] : kNowhere, off);
+                for (int v = 0; v < 2; ++v)     // (past the last row: past the buffer)
+                    w[u][g][v] = load_line(wb[g], thin_offset(lane, v, a.cols, left), off);
 #pragma unroll
             for (int v = 0; v < 2; ++v)
                 x[u][v] = load_line(xb, n < rows && 32 * c + 16 * v < left ? xo + 16u * v : kNowhere, off);

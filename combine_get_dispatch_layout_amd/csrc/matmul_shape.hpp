@@ -63,6 +63,49 @@ inline int64_t thin_tiles(bool gate, int64_t units, int64_t rows)
     return (rows + 15) / 16 * ((units + 15) / 16) * (gate ? 2 : 1);
 }
 
+// A lane offset past every buffer: reads 0.
+constexpr uint32_t kNowhere = 0x80000000u;
+
+// Group g of the thin kernel's block whose outputs begin at unit0: its first weight
+// row and how many it has.  A group behind the last output takes the block's first
+// (which is not stored twice): a buffer of no rows there is no bound, since the
+// hardware compares lane offsets with its size less the scalar offset, which wraps.
+struct ThinGroup {
+    int first, have;
+};
+constexpr ThinGroup thin_group(int unit0, int g, int units)
+{
+    const int u = unit0 + 16 * g < units ? unit0 + 16 * g : unit0;
+    return {u, units - u < 16 ? units - u : 16};
+}
+
+// Lane offset of weight load v (rows 8 v to 8 v + 7) of a line, of which `left`
+// columns are in the row.
+constexpr uint32_t thin_offset(int lane, int v, int cols, int left)
+{
+    return 16 * (lane >> 3) < left ? (uint32_t)(8 * v + (lane & 7)) * (uint32_t)cols + 16u * (lane >> 3) : kNowhere;
+}
+
+// One behind the last byte of a gateless matrix that the thin kernel's weight loads
+// can read with `groups` groups a block, taking the bound as it wraps.
+inline int64_t thin_reach(int groups, int cols, int units)
+{
+    int64_t most = 0;
+    const int lines = (cols + 127) / 128, outputs = 16 * groups, last = (units - 1) / outputs * outputs;
+    for (int unit0 = last >= outputs ? last - outputs : last; unit0 <= last; unit0 += outputs)
+        for (int g = 0; g < groups; ++g) {
+            const ThinGroup at = thin_group(unit0, g, units);
+            for (int line = 0; line < lines; ++line)
+                for (int i = 0; i < 128; ++i) {
+                    const uint32_t off = thin_offset(i / 2, i % 2, cols, cols - 128 * line), scalar = 128u * line;
+                    if (off >= (uint32_t)at.have * (uint32_t)cols - scalar) continue;
+                    const int64_t to = (int64_t)at.first * cols + off + scalar + 16;
+                    most = to > most ? to : most;
+                }
+        }
+    return most;
+}
+
 // cols, units of the weight matrix; experts: 0 for one matrix; rows: of all
 // experts.
 inline Path choose_path(bool gate, int64_t cols, int64_t units, int64_t experts, int64_t rows)

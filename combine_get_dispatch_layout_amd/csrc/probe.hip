@@ -239,3 +239,8 @@ extern "C" int ep_probe_matmul_splits(int gate, int64_t cols, int64_t units, int
 {
     return epk::mm::choose_splits(gate != 0, cols, units, rows);
 }
+
+extern "C" int64_t ep_probe_matmul_thin_reach(int groups, int cols, int units)
+{
+    return epk::mm::thin_reach(groups, cols, units);
+}

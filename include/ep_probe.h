@@ -91,6 +91,10 @@ int ep_probe_matmul_path(int gate, int64_t cols, int64_t units, int64_t experts,
  * rows and 64 weight rows; 1: it does as ep_matmul. */
 int ep_probe_matmul_splits(int gate, int64_t cols, int64_t units, int64_t rows);
 
+/* One behind the last byte of the weights (no gate) that EP_MATMUL_THIN's loads can
+ * read with `groups` groups of 16 outputs a block; host arithmetic only. */
+int64_t ep_probe_matmul_thin_reach(int groups, int cols, int units);
+
 #ifdef __cplusplus
 }
 #endif
