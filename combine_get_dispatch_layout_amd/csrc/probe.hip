@@ -211,7 +211,15 @@ int weight_kind(int format, int group)
 {
     if (format == EP_WEIGHT_BF16) return epk::kBf16;
     if (format == EP_WEIGHT_MXFP4) return epk::kMxfp4;
+    if (format == EP_WEIGHT_INT8) return epk::kInt8;
     return group == 32 ? epk::kInt4G32 : group == 64 ? epk::kInt4G64 : epk::kInt4G128;
+}
+
+epk::prod::Shape product_shape(int format, int group, int gate, int terms, int64_t cols, int64_t units,
+                               int64_t experts, int64_t rows)
+{
+    const int kind = weight_kind(format, group);
+    return epk::prod::choose_shape(kind, gate != 0, terms, kind == epk::kInt8 ? cols / 2 : cols, units, experts, rows);
 }
 
 }  // namespace
@@ -219,10 +227,15 @@ int weight_kind(int format, int group)
 extern "C" int ep_probe_product_path(int format, int group, int gate, int terms, int64_t cols, int64_t units,
                                      int64_t experts, int64_t rows, int64_t* rows_at_once)
 {
-    const epk::prod::Shape s =
-        epk::prod::choose_shape(weight_kind(format, group), gate != 0, terms, cols, units, experts, rows);
+    const epk::prod::Shape s = product_shape(format, group, gate, terms, cols, units, experts, rows);
     if (rows_at_once) *rows_at_once = s.rows;
     return s.path;
+}
+
+extern "C" int ep_probe_product_waves(int format, int group, int gate, int terms, int64_t cols, int64_t units,
+                                      int64_t experts, int64_t rows)
+{
+    return product_shape(format, group, gate, terms, cols, units, experts, rows).kw;
 }
 
 extern "C" int ep_probe_layer_in_two(int format, int group, int64_t tokens, int64_t topk, int64_t inter)

@@ -59,7 +59,8 @@ int ep_probe_rows(int mode, const void* d_src, void* d_dst, const int32_t* d_slo
  * arithmetic only.  format, group: of the weights; gate: 1 with EP_ACT_SWIGLU;
  * terms: 1, or 2 for a layer's down projection; units: outputs after the
  * activation; experts: 1 for ep_matvec; rows: num_rows, or num_tokens *
- * num_topk of the layout or layer. */
+ * num_topk of the layout or layer.  EP_WEIGHT_INT8: of a product that is
+ * EP_MATMUL_FEW. */
 enum {
     EP_PATH_NONE = 0,       /* no rows                                         */
     EP_PATH_SMALL = 1,      /* few tiles: blocks of four waves                 */
@@ -69,6 +70,10 @@ enum {
 };
 int ep_probe_product_path(int format, int group, int gate, int terms, int64_t cols, int64_t units,
                           int64_t experts, int64_t rows, int64_t* rows_at_once);
+
+/* How many waves share a tile's columns in that kernel. */
+int ep_probe_product_waves(int format, int group, int gate, int terms, int64_t cols, int64_t units,
+                           int64_t experts, int64_t rows);
 
 /* 1 if ep_moe_layer adds a token's experts inside the down projection (two
  * kernels), 0 if it takes three; format, group: w_down's. */
