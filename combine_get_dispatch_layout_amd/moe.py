@@ -275,10 +275,9 @@ class _BalanceLoss(torch.autograd.Function):
         out = ep_balance_loss(cfg, logits, topk_idx, token_mask, seq_start, loss, counts, seq_tokens,
                               score_sums, workspace)
         ctx.cfg, ctx.leaf = cfg, logits.is_leaf
-        # a given buffer may be filled again before the backward pass
-        ctx.save_for_backward(logits, token_mask, seq_start,
-                              out.counts if counts is None else out.counts.clone(),
-                              out.seq_tokens if seq_tokens is None else out.seq_tokens.clone())
+        # copies: before the backward pass the caller may fill a given buffer again,
+        # or sum the counts over ranks in place, which raises no version
+        ctx.save_for_backward(logits, token_mask, seq_start, out.counts.clone(), out.seq_tokens.clone())
         # outputs of their own, in the given memory: the buffers keep no graph
         out = [o if given is None else o.detach()
                for o, given in zip(out, (loss, counts, seq_tokens, score_sums))]
