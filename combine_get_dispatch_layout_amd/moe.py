@@ -4,13 +4,15 @@ loss, products with expert weights, whole expert layer), over torch tensors.
 As in ep.py: argument marshalling only, the functions carry the C names, the
 work is queued on the current stream of the tensors' device, and outputs are
 allocated with torch when none are passed.  ep_gate and ep_balance_loss take
-part in autograd; the other calls' outputs have no gradient.
+part in autograd (first order, reverse mode); the other calls' outputs have no
+gradient.
 """
 import ctypes
 from dataclasses import dataclass, field
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import ep
 from .ep import EP_OK, Handle, _check, lib
@@ -140,6 +142,14 @@ def _check_logits(cfg, logits):
     return logits.shape[0], logits.device
 
 
+def _records(name, logits):
+    """Whether autograd records a call on logits.  A tangent (forward mode) is
+    refused: it would be lost without a word."""
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(logits).tangent is not None:
+        raise RuntimeError(f"{name} has no forward mode derivative")
+    return logits.requires_grad and torch.is_grad_enabled()
+
+
 class _Gate(torch.autograd.Function):
     """ep_gate with ep_gate_backward as its weights' gradient."""
 
@@ -183,7 +193,7 @@ def ep_gate(cfg: GateConfig, logits: torch.Tensor, bias: Optional[torch.Tensor] 
     autograd records and the logits require a gradient, the returned weights
     have one, the choice held fixed (a topk_weights passed in is filled, but it
     is the returned tensor that has the gradient)."""
-    if logits.requires_grad and torch.is_grad_enabled():
+    if _records("ep_gate", logits):
         return _Gate.apply(cfg, logits, bias, token_mask, topk_idx, topk_weights)
     N, dev = _check_logits(cfg, logits)
     shape = (N, cfg.num_topk)
@@ -316,7 +326,7 @@ def ep_balance_loss(cfg: BalanceConfig, logits: torch.Tensor, topk_idx: torch.Te
     gradient, the returned loss has one (a loss passed in is filled, but it is
     the returned tensor that has the gradient).  workspace: uint8, at least
     ep_balance_workspace_size bytes (allocated for this call when not given)."""
-    if logits.requires_grad and torch.is_grad_enabled():
+    if _records("ep_balance_loss", logits):
         return Balance(*_BalanceLoss.apply(cfg, logits, topk_idx, token_mask, seq_start, loss, counts,
                                            seq_tokens, score_sums, workspace))
     N, dev = _check_logits(cfg, logits)

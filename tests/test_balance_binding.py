@@ -1,7 +1,8 @@
-"""CPU-only checks of the balance loss's autograd function, with stand-ins for the
-calls of the library."""
+"""CPU-only checks of the balance loss under autograd, with stand-ins for the calls
+of the library, and of what it and the router refuse there."""
 import pytest
 import torch
+import torch.autograd.forward_ad as fwAD
 
 from combine_get_dispatch_layout_amd import moe
 
@@ -38,3 +39,21 @@ def test_backward_has_the_counts_of_its_call(calls):
     counts, tokens, g = calls[0]
     assert (counts == 5).all() and (tokens == 7).all() and float(g) == 2
     assert (lg.grad == 1).all()
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_forward_mode_is_refused(grad):
+    """Neither call has a tangent to give; none is lost without a word."""
+    idx = torch.zeros((4, 2), dtype=torch.int32)
+    with fwAD.dual_level():
+        lg = fwAD.make_dual(torch.zeros((4, 16), requires_grad=grad), torch.ones(4, 16))
+        with pytest.raises(RuntimeError, match="ep_balance_loss has no forward"):
+            moe.ep_balance_loss(moe.BalanceConfig(16, 2), lg, idx)
+        with pytest.raises(RuntimeError, match="ep_gate has no forward"):
+            moe.ep_gate(moe.GateConfig(16, 2), lg)
+        with torch.no_grad(), pytest.raises(RuntimeError, match="ep_gate has no forward"):
+            moe.ep_gate(moe.GateConfig(16, 2), lg)
+        with pytest.raises(ValueError, match="on the GPU"):        # without a tangent: as ever
+            moe.ep_gate(moe.GateConfig(16, 2), torch.zeros(4, 16))
+    with pytest.raises(ValueError, match="on the GPU"):
+        moe.ep_gate(moe.GateConfig(16, 2), torch.zeros(4, 16))

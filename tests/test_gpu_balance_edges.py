@@ -1,5 +1,4 @@
-"""GPU tests of the balance loss where a caller changes what it returned, and of
-its gradient for tokens that are all but sure of one expert."""
+"""GPU tests of the balance loss where a caller changes what it returned."""
 import pytest
 import torch
 
