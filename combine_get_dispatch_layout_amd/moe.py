@@ -474,11 +474,17 @@ def _check_x_scales(x, x_scales):
         _check_tensor("x_scales", x_scales, (torch.float32,), (x.shape[0],), x.device)
 
 
+# Sizes that one Weights remembers: a server's batches have any number of rows.
+_MAX_SIZES = 256
+
+
 def ep_matmul_workspace_size(w: Weights, rows: int, activation: int = EP_ACT_NONE) -> int:
     n = w._workspace.get((rows, activation))
     if n is None:
         out = ctypes.c_int64()
         _check(_lib().ep_matmul_workspace_size(w._ref, rows, activation, ctypes.byref(out)))
+        if len(w._workspace) >= _MAX_SIZES:
+            w._workspace.clear()
         n = w._workspace[rows, activation] = out.value
     return n
 
