@@ -445,7 +445,11 @@ __global__ __launch_bounds__(kFinishWaves* kWave) void k_balance_finish(BalanceA
 //   normalised sigmoid  p (1 - s) (f - sum f p)
 // Scores that sum to one leave a constant in f without effect: K T / E, what
 // every expert has of a balanced batch, is taken from the counts as an integer,
-// so that the differences do not drown in the counts' own size.
+// so that the differences do not drown in the counts' own size.  A token with most
+// of its score on one expert measures the counts from that expert's: sum f p all but
+// equals its f, and their difference, which the others' small scores make, would be
+// the rounding of f.  (65536 tokens of 256 experts, fp32, softmax: 32.3 us, 31.7
+// without; if most tokens are so sure 33.1.)
 template <int LANES, int VECS, int FORM>
 __global__ __launch_bounds__(kThreads) void k_balance_backward(BalanceArgs a)
 {
@@ -507,17 +511,35 @@ __global__ __launch_bounds__(kThreads) void k_balance_backward(BalanceArgs a)
         }
         if (in) {
             const float by = X::template scores<true>(a, z, rest);
-            float dot = 0.f;
-            if (divide) {
-#pragma unroll
-                for (int i = 0; i < X::kEach; ++i) dot = fmaf(z[i], f[i], dot);
-                dot = lanes_sum<LANES>(dot) * by;
-            }
             const float all = by * scale;
+            // z becomes p (f - c - sum (f - c) p) for a number c of the token's
+            auto slope = [&](auto from) {
+                float dot = 0.f;
+                if (divide) {
 #pragma unroll
-            for (int i = 0; i < X::kEach; ++i) {
-                z[i] *= (f[i] - dot) * all;
-                if (a.scoring != 0) z[i] *= rest[i];
+                    for (int i = 0; i < X::kEach; ++i) dot = fmaf(z[i], from(f[i]), dot);
+                    dot = lanes_sum<LANES>(dot) * by;
+                }
+#pragma unroll
+                for (int i = 0; i < X::kEach; ++i) {
+                    z[i] *= (from(f[i]) - dot) * all;
+                    if (a.scoring != 0) z[i] *= rest[i];
+                }
+            };
+            // (scores before `by` are at most 1; one branch for the wave's tokens)
+            const bool sure = divide && by > 0.5f;
+            if (__builtin_expect(__any(sure), 0)) {
+                float most = 0.f, c = kLow;
+#pragma unroll
+                for (int i = 0; i < X::kEach; ++i) most = fmaxf(most, z[i]);
+                most = lanes_max<LANES>(most);
+#pragma unroll
+                for (int i = 0; i < X::kEach; ++i) c = fmaxf(c, z[i] == most ? f[i] : kLow);
+                c = lanes_max<LANES>(c);
+                if (!sure) c = 0.f;
+                slope([c](float v) { return v - c; });
+            } else {
+                slope([](float v) { return v; });
             }
         } else {
 #pragma unroll
