@@ -9,9 +9,10 @@
 // What bounds it: one reading of the logits (the gradient: and one writing) and
 // some 17 instructions a score, two of them at a quarter of the rate, which take as
 // long; for small batches the launches.  65536 tokens of 256 experts, fp32, sigmoid
-// scores in 37 sequences: 18 us and 9 for the second kernel, 27 in all (the bytes
-// at the rate of a large read: 9.6); the gradient 34 (the bytes at the rate of a
-// copy: 29).  4096 tokens of 128 experts, bf16: 3.8, 6.7 and 4.1 us.
+// scores in 37 sequences: 19 us and 9 for the second kernel, 28 in all (the bytes
+// at the rate of a large read: 9.6); the gradient 35 (a plain copy of the same
+// bytes: 23).  In bf16, softmax scores: 25.6 in all, the gradient 21.  4096 tokens
+// of 128 experts, bf16: 3.8, 6.4 and 4.0 us.
 //
 // A token's experts lie in 16 lanes (64 above 256 experts), sixteen or fewer to
 // a lane: a reduction over them is four steps inside a row of lanes, for four
@@ -361,7 +362,9 @@ __device__ __forceinline__ int wave_total(int v)
 // of the loss, in their order.  What bounds it is a chain of loads, and with many
 // blocks their way past the one counter, 23 ns each: 65536 tokens of 256 experts in
 // 1024 sequences took 131 us with a block an item, 29 with at most 256 blocks (both
-// kernels), in 8192 sequences 807 and 60.
+// kernels), in 8192 sequences 807 and 60.  `join` goes by the mean of pieces a
+// sequence, so one long sequence beside many others is walked by few waves: 65536
+// tokens in one sequence 32 us, with 1024 empty ones beside it 98.
 __global__ __launch_bounds__(kFinishWaves* kWave) void k_balance_finish(BalanceArgs a, int slices, int join)
 {
     __shared__ double sums[kFinishWaves][kWave];

@@ -40,10 +40,11 @@
 // has room for the sums, which a second kernel joins (choose_splits).
 //
 // What bounds it.  One matrix: power, and behind that the way through LDS; 4096
-// rows, 7168 -> 4096, 96 to 105 us at 1.8 to 2.1 GHz of 2.4, 2.3 to 2.5 POP/s (the
-// library's plain products: 2.1 to 2.2).  Experts: the way of their columns from L2
-// to LDS, some 16 TB/s over the chip, and of the outputs to memory, which all CUs
-// write at once: 64 experts of 768 rows, 1536 -> 4096, 375 us, without the stores
+// rows, 7168 -> 4096, 96 to 101 us, 2.4 to 2.5 POP/s (the library's plain products:
+// 2.1 to 2.2), launches without a pause 113 at 2.1 GHz of 2.4.  Experts: the way of
+// their columns from L2 to LDS (128 experts of 256 rows, 2048 -> 2 x 768: 3840 tiles
+// of 16 stages of 32 KB, 2.0 GB in 165 us), and of the outputs to memory, which all
+// CUs write at once: 64 experts of 768 rows, 1536 -> 4096, 375 us, without the stores
 // 305, loads alone 257.
 #include "experts.hpp"
 #include "matmul_shape.hpp"
@@ -238,7 +239,7 @@ __global__ __launch_bounds__(64 * WM * WN, (WM * WN / 4 * Tile<BM, BN, WM, WN, S
 {
     using T = Tile<BM, BN, WM, WN, S, GATE>;
     constexpr int MT = T::MT, NT = T::NT;
-    extern __shared__ __align__(1024) unsigned char smem[];     // stages, scales of two tiles
+    extern __shared__ __align__(1024) unsigned char smem[];     // stages, scales of kScales tiles
     __shared__ Tiles tiles;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);

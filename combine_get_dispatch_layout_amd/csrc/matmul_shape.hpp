@@ -28,6 +28,10 @@ constexpr int stages(Path p) { return p == kPathTile64x64 ? 4 : p == kPathTile64
 constexpr int scale_buffers(int S) { return S == 2 ? 3 : 2; }
 constexpr bool enough_steps(Path p, int64_t steps) { return (scale_buffers(stages(p)) - 1) * steps > stages(p) - 1; }
 
+// All figures of this choice, the number of blocks at once and the band of the thin
+// kernel's pairs among them, are for 256 CUs.  On another number every call is right
+// all the same: only the launches, which take the CUs that there are, differ.
+//
 // The tiled kernels' time, in steps of a 256 x 256 tile (1.8 us): a step of a
 // round of tiles (one or two blocks to each CU) and what a round costs beside its
 // steps.  Measured, in us, with 7168 columns and no gate where one expert:

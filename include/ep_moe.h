@@ -231,7 +231,8 @@ ep_status ep_expert_matvec(const ep_handle* h, const ep_weights* w, const void* 
  *   ep_quantize_rows'; all 256 codes are values.  d_y bf16 [num_rows, M] (or
  *   [num_rows, M/2] with EP_ACT_SWIGLU), not overlapping x.
  *   Sums are exact; a sum, rounded to fp32, is multiplied by its row's scale, then
- *   by its output's, in fp32, and after the activation rounded to bf16 once.
+ *   by its output's, in fp32, and after the activation rounded to bf16 once.  The
+ *   silu of a gate below -88.72, less than 2^-121, is -0.
  *   num_rows * M below 2^35. */
 ep_status ep_matmul(const ep_weights* w, const void* d_x, const float* d_x_scales,
                     int64_t num_rows, int32_t activation, void* d_y, void* stream);
@@ -252,7 +253,11 @@ ep_status ep_matmul_split(const ep_weights* w, const void* d_x, const float* d_x
 
 /* The same for received rows, each with its expert's matrix: rows, layout, flags
  * and states as ep_expert_matvec; the scales of rows that hold no token are not
- * read either. */
+ * read either.
+ *   The kernel is chosen by the mean, num_tokens * num_topk over the experts: a
+ *   mean of up to 8 rows can go to kernels that read a matrix once for each 16 of
+ *   its rows (ep_probe_matmul_path tells), which costs time where a batch's tokens
+ *   agree on few of many experts; the result is the same. */
 ep_status ep_expert_matmul(const ep_handle* h, const ep_weights* w, const void* d_x,
                            const float* d_x_scales, int64_t x_rows, int32_t activation, void* d_y,
                            void* stream);

@@ -84,7 +84,8 @@ int ep_probe_layer_in_two(int format, int group, int64_t tokens, int64_t topk, i
 enum {
     EP_MATMUL_NONE = 0,         /* no rows                                     */
     EP_MATMUL_FEW = 1,          /* the kernels of ep_probe_product_path        */
-    EP_MATMUL_THIN = 2,         /* blocks of 16 rows and 16 outputs            */
+    EP_MATMUL_THIN = 2,         /* blocks of 16 rows and 16 outputs, or 32 where
+                                   448 to 512 tiles of 16 x 16 make the product */
     EP_MATMUL_TILE64X64 = 3,    /* tiles of rows of x and weight rows          */
     EP_MATMUL_TILE64X128 = 4,
     EP_MATMUL_TILE128 = 5,
