@@ -78,3 +78,39 @@ def test_sure_tokens(score, E):
                            err[sure][bad][:4])
     r = np.arange(N)
     assert np.median((err / np.maximum(np.abs(want), 1e-300))[r, top]) < 2.0 ** -15      # the bound tells
+
+
+def test_captured_step_through_autograd():
+    """Loss and gradient of logits that are no leaf in one graph, each replay against
+    the eager calls, with eager work between."""
+    N, E, K, Q = 600, 64, 4, 3
+    cfg = moe.BalanceConfig(E, K)
+    w = torch.randn((N, E), device="cuda", requires_grad=True)
+    idx = torch.randint(-1, E, (N, K), dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 100, 400, 590], dtype=torch.int32, device="cuda")
+
+    def step():
+        lg = w * 2
+        out = moe.ep_balance_loss(cfg, lg, idx, None, start)
+        return out.loss.detach(), out.counts, torch.autograd.grad(out.loss, lg)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for i in range(5):
+        with torch.no_grad():
+            w.normal_()
+        idx.random_(-1, E)
+        start[1:3] += 5
+        for t in got:
+            t.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), i
